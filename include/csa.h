@@ -63,9 +63,15 @@ typedef enum {
   CSA_FP8_E4M3_ROWSCALE = 2, /* OCP e4m3 codes, one fp32 scale per row (value = code * scale) */
   CSA_MXFP4 = 3,             /* OCP MXFP4: e2m1 pairs per byte (element 2j in the low nibble)
                                 and one e8m0 scale byte per 32 elements */
-  CSA_MIXED_FP8_BF16 = 4     /* KV entry row ([P1] 一(三)4 item 1): the first c-r values as e4m3
+  CSA_MIXED_FP8_BF16 = 4,    /* KV entry row ([P1] 一(三)4 item 1): the first c-r values as e4m3
                                 codes with one fp32 scale per row (amax of those values / 448),
                                 then the last r (RoPE) values as bf16: c + r bytes per row */
+  CSA_MIXED_MXFP4_BF16 = 5   /* KV entry row in about four bits a value, one record per row and
+                                no separate scales: the first c-r values as e2m1 pairs
+                                ((c-r)/2 bytes, element 2j in the low nibble), one e8m0 exponent
+                                floor(log2 amax) - 2 per 32 of them, held to [-14, 13] and padded
+                                with zero bytes to a multiple of 16, then the last r (RoPE)
+                                values as bf16. 368 bytes at c = 512, r = 64; r a multiple of 32 */
 } csa_dtype;
 
 /* Method constants, passed by pointer, read on the host during the call only. */
@@ -146,7 +152,9 @@ csa_status csa_compress(const csa_params* p, csa_dtype io, int32_t B, int64_t n_
  *         16*i + 4*j + b holding exponent b of row 32*j + i;
  *       CSA_MIXED_FP8_BF16 (0 < r < c): pages [n_pages, page_rows, c + r] bytes, each row the
  *         e4m3 codes of its first c-r values then its last r values as bf16; page_scales
- *         [n_pages, page_rows] fp32 = amax(first c-r values) / 448.
+ *         [n_pages, page_rows] fp32 = amax(first c-r values) / 448;
+ *       CSA_MIXED_MXFP4_BF16 (0 < r < c, r a multiple of 32): pages [n_pages, page_rows, row
+ *         bytes] as csa_dtype gives them; page_scales unused.
  *     Indexer keys are compressed like KV entries but take no RMSNorm / RoPE (finalize = 0).
  * The slots of block i-1 and block i are read back, so a request's appends must arrive in
  * position order (one per call), after its state was filled up to t-1: by earlier appends,
@@ -298,8 +306,9 @@ csa_status hca_dense_mqa_mixed_kv(const csa_params* p, int32_t B, int32_t T, con
  * N_cap = page_rows * max_pages. Passed by pointer, read on the host during the call.
  */
 typedef struct {
-  csa_dtype fmt;              /* CSA_BF16 (pages [n_pages, page_rows, c]) or CSA_MIXED_FP8_BF16
-                                 (pages [n_pages, page_rows, c + r] bytes)                  */
+  csa_dtype fmt;              /* CSA_BF16 (pages [n_pages, page_rows, c]), CSA_MIXED_FP8_BF16
+                                 (pages [n_pages, page_rows, c + r] bytes) or
+                                 CSA_MIXED_MXFP4_BF16 (pages [n_pages, page_rows, 368] bytes) */
   const void* pages;          /* device                                                     */
   const void* scales;         /* CSA_MIXED_FP8_BF16 and CSA_FP8_E4M3_ROWSCALE: fp32
                                  [n_pages, page_rows]; CSA_MXFP4 keys: the e8m0 exponent
@@ -312,11 +321,15 @@ typedef struct {
  * Stage 4 over a paged cache: as csa_sparse_mqa / hca_dense_mqa with io = CSA_BF16 (the
  * mixed format as in csa_sparse_mqa_mixed_kv), reading each cache row through the page
  * table. An entry whose page id lies outside [0, n_pages) is skipped and leaves device
- * error code 205 for csa_device_error(). The window may be the state cache's ring
+ * error code 205 (4-bit rows: 216) for csa_device_error(); one whose table entry is -2 (its
+ * page was evicted, csa_evict_pages) is skipped without one. The window may be the state cache's ring
  * (csa_state_append's win_ring): pass win_pos0 = NULL and L_raw = n_win, one query per
  * request (T = 1); window position p is then read from row p mod n_win. Tensor-core attention only (c = 512, n_heads a
  * multiple of 64; mixed rows: rope_dims a multiple of 16 in (0, 512)), else
  * CSA_ERR_UNSUPPORTED. Workspace: csa_workspace_size() with N_cap = page_rows * max_pages.
+ * 4-bit rows (fmt = CSA_MIXED_MXFP4_BF16; rope_dims = 64, else CSA_ERR_UNSUPPORTED) take the
+ * workspace of kdt = CSA_MIXED_MXFP4_BF16. Their operands are f16 (window and RoPE values up to
+ * 65504 in magnitude; a larger one becomes infinite), the sums fp32.
  */
 csa_status csa_sparse_mqa_paged(const csa_params* p, int32_t B, int32_t T, const void* q,
                                 const int64_t* q_pos, const csa_paged_kv* kv, const int32_t* idx,
@@ -432,7 +445,8 @@ int32_t csa_state_pages_needed(int32_t m, int32_t page_rows, int64_t n_tok);
  * first_entry .. first_entry + n - 1 of every request, stored in out_pages->fmt exactly as
  * csa_state_append stores a finished row: the io dtype, CSA_FP8_E4M3_ROWSCALE (scales fp32
  * [n_pages, page_rows]), CSA_MXFP4 (c = 128, page_rows a multiple of 128; exponent blocks
- * as for csa_state_append) or CSA_MIXED_FP8_BF16 (0 < p->rope_dims < c). This is the
+ * as for csa_state_append), CSA_MIXED_FP8_BF16 (0 < p->rope_dims < c) or CSA_MIXED_MXFP4_BF16
+ * (scales NULL). This is the
  * prefill -> decode hand-over for pools kept in a quantised format ([P1''] 二(六); [P1']
  * 二(四) for the FP4 indexer keys). An entry whose page id lies outside the pool is skipped
  * and leaves device error code 325 (324: its logical page is past the table, which the host
@@ -478,7 +492,9 @@ csa_status csa_forward(const csa_params* p, csa_dtype io, int32_t B, int32_t T,
 
 /*
  * Bytes of workspace the call `entry` needs for these sizes (0 if none). Returns 0 and
- * sets csa_last_error() on invalid sizes. kdt: the indexer key format (for the index calls).
+ * sets csa_last_error() on invalid sizes. kdt: the indexer key format (for the index and forward
+ * calls); for CSA_WS_SPARSE_MQA and CSA_WS_HCA_MQA CSA_MIXED_MXFP4_BF16 sizes the attention over
+ * 4-bit rows and any other value the one over bf16 / FP8 rows.
  */
 size_t csa_workspace_size(const csa_params* p, int32_t entry, csa_dtype kdt, int32_t B,
                           int32_t T, int64_t N_cap);
@@ -525,7 +541,8 @@ void csa_set_index_timing_events(void* const* before, void* const* after, int32_
  * a wait that runs out stores a nonzero code (the first one wins) and the kernel returns
  * early instead of hanging. csa_state_append also leaves a code for a request it skipped.
  * Codes by kernel family: 101-107 MXFP4 indexer (107: a page id outside the pool), 201-205
- * attention (205: a page id outside the pool), 301-309 FP8 / bf16 indexer (309: a page id
+ * attention (205: a page id outside the pool), 211-216 attention over 4-bit rows (216: a page id
+ * outside the pool), 301-309 FP8 / bf16 indexer (309: a page id
  * outside the pool), 321-323 state append, 324-325 encoding into pages, 331 paged
  * compression, 401-405 prefill output projection. Writes the code to *code (0 = none) and clears it. Synchronises the device.
  * Returns CSA_ERR_CUDA if the copy fails.

@@ -16,7 +16,8 @@ LIB_PATH = os.path.join(HERE, "libcsa.so")
 
 (CSA_OK, CSA_ERR_INVALID_ARG, CSA_ERR_UNSUPPORTED, CSA_ERR_WORKSPACE, CSA_ERR_CUDA,
  CSA_ERR_NO_PAGES) = range(6)
-CSA_F32, CSA_BF16, CSA_FP8_E4M3_ROWSCALE, CSA_MXFP4, CSA_MIXED_FP8_BF16 = range(5)
+(CSA_F32, CSA_BF16, CSA_FP8_E4M3_ROWSCALE, CSA_MXFP4, CSA_MIXED_FP8_BF16,
+ CSA_MIXED_MXFP4_BF16) = range(6)
 DTYPES = {"f32": CSA_F32, "bf16": CSA_BF16, "fp8": CSA_FP8_E4M3_ROWSCALE, "mxfp4": CSA_MXFP4}
 (CSA_WS_INDEX_TOPK, CSA_WS_TOPK, CSA_WS_SPARSE_MQA, CSA_WS_HCA_MQA, CSA_WS_FORWARD,
  CSA_WS_INDEX_TOPK_BF16) = range(1, 7)

@@ -1,5 +1,6 @@
 // C ABI of libcsa (declared in include/csa.h): host-side validation, workspace layout and
 // dispatch to the stage kernels. Nothing is launched unless every argument checks out.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -87,6 +88,13 @@ csa_status check_index(const csa_params* p, csa_dtype kdt) {
 csa_status check_topk(const csa_params* p) {
   REQUIRE(p->topk >= 1 && p->topk <= csa::kMaxTopk, "topk must be in [1, %d] (got %d)",
           csa::kMaxTopk, p->topk);
+  return CSA_OK;
+}
+
+// 4-bit KV rows: whole MX blocks before the RoPE values
+csa_status check_fp4_rows(const csa_params* p) {
+  REQUIRE(p->rope_dims > 0 && p->rope_dims < p->c && p->rope_dims % 32 == 0,
+          "4-bit KV rows need 0 < rope_dims < c and rope_dims a multiple of 32");
   return CSA_OK;
 }
 
@@ -179,6 +187,12 @@ csa_status check_index_args(const csa_params* p, csa_dtype kdt, int32_t B, int32
   return CSA_OK;
 }
 
+// workspace of the attention over bf16 / FP8 rows, or over 4-bit rows
+size_t attn_bytes(const csa::MqaArgs& a, bool fp4) {
+  if (!fp4) return csa::mqa_workspace_bytes(a);
+  return csa::attn_fp4_supported(a) ? csa::attn_fp4_workspace_bytes(a) : 0;
+}
+
 // csa_forward with the tensor-core attention: the top-k kernel also prepares the
 // attention's q_hat (bf16 [B*T][H][c]) in the workspace
 bool forward_qhat(const csa_params* p, int32_t B, int32_t T, int64_t N_cap) {
@@ -259,13 +273,14 @@ const char* csa_last_error(void) { return g_err; }
 
 csa_status csa_device_error(int32_t* code) {
   REQUIRE(code != nullptr, "code is NULL");
-  int words[6] = {0, 0, 0, 0, 0, 0};
+  int words[7] = {0, 0, 0, 0, 0, 0, 0};
   TRY(cuda_status(csa::index_mxf4_device_error(&words[0]), "device error word"));
   TRY(cuda_status(csa::mqa_tc_device_error(&words[1]), "device error word"));
   TRY(cuda_status(csa::index_bf16_device_error(&words[2]), "device error word"));
   TRY(cuda_status(csa::state_append_device_error(&words[3]), "device error word"));
   TRY(cuda_status(csa::out_proj_tc_device_error(&words[4]), "device error word"));
   TRY(cuda_status(csa::compress_device_error(&words[5]), "device error word"));
+  TRY(cuda_status(csa::attn_fp4_device_error(&words[6]), "device error word"));
   *code = 0;
   for (int w : words)
     if (*code == 0) *code = w;
@@ -298,7 +313,7 @@ void csa_set_index_timing_events(void* const* before, void* const* after, int32_
 size_t csa_workspace_size(const csa_params* p, int32_t entry, csa_dtype kdt, int32_t B,
                           int32_t T, int64_t N_cap) {
   if (check_params(p) != CSA_OK || check_sizes(B, T, N_cap) != CSA_OK) return 0;
-  (void)kdt;
+  const bool fp4 = kdt == CSA_MIXED_MXFP4_BF16;  // the attention entries' cache format
   const size_t topk_ws = round_up(csa::topk_workspace_bytes(B, T, N_cap, p->topk));
   csa::MqaArgs m = make_mqa(p, B, T, nullptr, nullptr, nullptr, N_cap, nullptr, p->topk,
                             nullptr, 0, nullptr, nullptr, nullptr, nullptr);
@@ -310,13 +325,14 @@ size_t csa_workspace_size(const csa_params* p, int32_t entry, csa_dtype kdt, int
     case CSA_WS_TOPK:
       return topk_ws;
     case CSA_WS_SPARSE_MQA:
-      return round_up(csa::mqa_workspace_bytes(m));
+      return round_up(attn_bytes(m, fp4));
     case CSA_WS_HCA_MQA:
       m.k = 0;
-      return round_up(csa::mqa_workspace_bytes(m));
-    case CSA_WS_FORWARD:
-      return scores_bytes(B, T, N_cap) + topk_ws + round_up(csa::mqa_workspace_bytes(m)) +
-             qhat_bytes(p, B, T, N_cap);
+      return round_up(attn_bytes(m, fp4));
+    case CSA_WS_FORWARD: {  // kdt names the keys here: room for the attention of any KV format
+      const size_t any = std::max(attn_bytes(m, false), attn_bytes(m, true));
+      return scores_bytes(B, T, N_cap) + topk_ws + round_up(any) + qhat_bytes(p, B, T, N_cap);
+    }
     default:
       fail(CSA_ERR_INVALID_ARG, "unknown workspace entry %d", entry);
       return 0;
@@ -436,12 +452,14 @@ csa_status csa_state_append(const csa_params* p, csa_dtype io, int32_t B, const 
   REQUIRE(io == CSA_F32 || io == CSA_BF16, "state io dtype must be CSA_F32 or CSA_BF16");
   REQUIRE(p->c <= 4096, "state append supports c <= 4096 (got %d)", p->c);
   REQUIRE(out_fmt == io || out_fmt == CSA_FP8_E4M3_ROWSCALE || out_fmt == CSA_MXFP4 ||
-              out_fmt == CSA_MIXED_FP8_BF16,
-          "out_fmt must be the io dtype, CSA_FP8_E4M3_ROWSCALE, CSA_MXFP4 or CSA_MIXED_FP8_BF16");
+              out_fmt == CSA_MIXED_FP8_BF16 || out_fmt == CSA_MIXED_MXFP4_BF16,
+          "out_fmt must be the io dtype, CSA_FP8_E4M3_ROWSCALE, CSA_MXFP4, CSA_MIXED_FP8_BF16 or "
+          "CSA_MIXED_MXFP4_BF16");
   if (out_fmt == CSA_MIXED_FP8_BF16)
     REQUIRE(p->rope_dims > 0 && p->rope_dims < p->c && p->rope_dims % 16 == 0,
             "mixed rows need 0 < rope_dims < c and rope_dims a multiple of 16 (16-byte "
             "aligned rows, as the attention over mixed rows reads them)");
+  if (out_fmt == CSA_MIXED_MXFP4_BF16) TRY(check_fp4_rows(p));
   if (out_fmt == CSA_MXFP4) {
     REQUIRE(p->c == 128, "MXFP4 rows are indexer keys of 128 values (c = %d)", p->c);
     REQUIRE(page_rows % 128 == 0, "MXFP4 pages hold whole 128-row exponent blocks");
@@ -468,7 +486,7 @@ csa_status csa_state_append(const csa_params* p, csa_dtype io, int32_t B, const 
   REQUIRE_PTR(state);
   REQUIRE_PTR(pages);
   REQUIRE_PTR(page_table);
-  if (out_fmt != io) REQUIRE_PTR(page_scales);
+  if (out_fmt != io && out_fmt != CSA_MIXED_MXFP4_BF16) REQUIRE_PTR(page_scales);
   OPTIONAL_PTR(win_row);
   OPTIONAL_PTR(win_ring);
   OPTIONAL_PTR(kv_rms_w);
@@ -482,7 +500,8 @@ csa_status csa_state_append(const csa_params* p, csa_dtype io, int32_t B, const 
   a.out = out_fmt == io                   ? csa::state::kOutIo
           : out_fmt == CSA_MXFP4          ? csa::state::kOutMxfp4
           : out_fmt == CSA_MIXED_FP8_BF16 ? csa::state::kOutMixed
-                                          : csa::state::kOutFp8;
+          : out_fmt == CSA_MIXED_MXFP4_BF16 ? csa::state::kOutMixedFp4
+                                            : csa::state::kOutFp8;
   for (int i = 0; i < p->rope_dims / 2; ++i)
     a.inv_freq[i] = csa::rope_inv_freq(i, p->rope_dims, (double)p->rope_base);
   TRY(cuda_status(csa::launch_state_append(a, io == CSA_BF16, (cudaStream_t)stream),
@@ -499,13 +518,14 @@ csa_status csa_encode_paged(const csa_params* p, csa_dtype io, int32_t B, int64_
   REQUIRE(out_pages != nullptr, "page descriptor is NULL");
   const csa_dtype fmt = out_pages->fmt;
   REQUIRE(fmt == io || fmt == CSA_FP8_E4M3_ROWSCALE || fmt == CSA_MXFP4 ||
-              fmt == CSA_MIXED_FP8_BF16,
-          "page format must be the io dtype, CSA_FP8_E4M3_ROWSCALE, CSA_MXFP4 or "
-          "CSA_MIXED_FP8_BF16");
+              fmt == CSA_MIXED_FP8_BF16 || fmt == CSA_MIXED_MXFP4_BF16,
+          "page format must be the io dtype, CSA_FP8_E4M3_ROWSCALE, CSA_MXFP4, "
+          "CSA_MIXED_FP8_BF16 or CSA_MIXED_MXFP4_BF16");
   if (fmt == CSA_MIXED_FP8_BF16)
     REQUIRE(p->rope_dims > 0 && p->rope_dims < p->c && p->rope_dims % 16 == 0,
             "mixed rows need 0 < rope_dims < c and rope_dims a multiple of 16 (16-byte "
             "aligned rows, as the attention over mixed rows reads them)");
+  if (fmt == CSA_MIXED_MXFP4_BF16) TRY(check_fp4_rows(p));
   if (fmt == CSA_MXFP4) {
     REQUIRE(p->c == 128, "MXFP4 rows are indexer keys of 128 values (c = %d)", p->c);
     REQUIRE(out_pages->page_rows % 128 == 0, "MXFP4 pages hold whole 128-row exponent blocks");
@@ -522,7 +542,7 @@ csa_status csa_encode_paged(const csa_params* p, csa_dtype io, int32_t B, int64_
   REQUIRE_PTR(rows);
   REQUIRE_PTR(out_pages->pages);
   REQUIRE_PTR(out_pages->page_table);
-  if (fmt != io) REQUIRE_PTR(out_pages->scales);
+  if (fmt != io && fmt != CSA_MIXED_MXFP4_BF16) REQUIRE_PTR(out_pages->scales);
   csa::state::Args a{};
   a.B = B; a.m = p->m; a.c = p->c; a.overlap = p->overlap; a.rope_dims = p->rope_dims;
   a.n_pages = out_pages->n_pages; a.page_rows = out_pages->page_rows;
@@ -533,7 +553,8 @@ csa_status csa_encode_paged(const csa_params* p, csa_dtype io, int32_t B, int64_
   a.out = fmt == io                   ? csa::state::kOutIo
           : fmt == CSA_MXFP4          ? csa::state::kOutMxfp4
           : fmt == CSA_MIXED_FP8_BF16 ? csa::state::kOutMixed
-                                      : csa::state::kOutFp8;
+          : fmt == CSA_MIXED_MXFP4_BF16 ? csa::state::kOutMixedFp4
+                                        : csa::state::kOutFp8;
   TRY(cuda_status(csa::launch_encode_paged(a, io == CSA_BF16, rows, n, first_entry,
                                            (cudaStream_t)stream), "encode into pages"));
   return ok();
@@ -809,12 +830,35 @@ csa_status hca_dense_mqa(const csa_params* p, csa_dtype io, int32_t B, int32_t T
 namespace {
 // Tensor-core attention over mixed-precision and / or paged cache rows.
 struct KvLayout {
-  bool mixed;
+  bool mixed, fp4;
   const void* rows;            // contiguous cache [B, N_cap, ...] or page pool
   const float* scales;         // mixed: per-row scales (same indexing as rows)
   const int32_t* page_table;   // paged: [B, max_pages]; NULL: contiguous
   int32_t n_pages, page_rows, max_pages;
 };
+
+void set_pages(csa::MqaArgs* a, const KvLayout& kv) {
+  a->page_table = kv.page_table;
+  a->n_pages = kv.n_pages;
+  a->page_rows = kv.page_rows;
+  a->max_pages = kv.max_pages;
+}
+
+// the attention over 4-bit rows: checked arguments, its shape and workspace, the launch
+csa_status fp4_mqa(const char* what, csa::MqaArgs a, const KvLayout& kv, void* ws,
+                   size_t ws_bytes, void* stream) {
+  if (!csa::attn_fp4_supported(a))
+    return fail(CSA_ERR_UNSUPPORTED,
+                "%s: 4-bit rows need c = 512, rope_dims = 64 and n_heads a multiple of 64", what);
+  set_pages(&a, kv);
+  a.fp4 = true;
+  const size_t need = csa::attn_fp4_workspace_bytes(a);
+  if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned16(ws)))
+    return fail(CSA_ERR_WORKSPACE, "%s needs %zu workspace bytes", what, need);
+  return cuda_status(csa::launch_attn_fp4(a, ws, ws_bytes, (cudaStream_t)stream), what) == CSA_OK
+             ? ok()
+             : CSA_ERR_CUDA;
+}
 
 csa_status tc_mqa_ext(const char* what, const csa_params* p, int32_t B, int32_t T,
                       const void* q, const int64_t* q_pos, const KvLayout& kv, int64_t N_cap,
@@ -829,6 +873,7 @@ csa_status tc_mqa_ext(const char* what, const csa_params* p, int32_t B, int32_t 
   if (kv.page_table != nullptr) REQUIRE_PTR(kv.page_table);
   auto a = make_mqa(p, B, T, q, q_pos, kv.rows, N_cap, idx, k, win_kv, L_raw, win_pos0, sink,
                     q_rms_w, out);
+  if (kv.fp4) return fp4_mqa(what, a, kv, ws, ws_bytes, stream);
   const bool rope_ok = !kv.mixed ||
                        (p->rope_dims > 0 && p->rope_dims < p->c && p->rope_dims % 16 == 0);
   if (!rope_ok || !csa::mqa_tc_supported(a, true))
@@ -851,15 +896,16 @@ csa_status tc_mqa_ext(const char* what, const csa_params* p, int32_t B, int32_t 
 
 csa_status paged_layout(const csa_paged_kv* kv, KvLayout* out, int64_t* N_cap) {
   REQUIRE(kv != nullptr, "paged KV descriptor is NULL");
-  REQUIRE(kv->fmt == CSA_BF16 || kv->fmt == CSA_MIXED_FP8_BF16,
-          "paged KV format must be CSA_BF16 or CSA_MIXED_FP8_BF16");
+  REQUIRE(kv->fmt == CSA_BF16 || kv->fmt == CSA_MIXED_FP8_BF16 ||
+              kv->fmt == CSA_MIXED_MXFP4_BF16,
+          "paged KV format must be CSA_BF16, CSA_MIXED_FP8_BF16 or CSA_MIXED_MXFP4_BF16");
   REQUIRE(kv->n_pages >= 1 && kv->page_rows >= 1 && kv->max_pages >= 1,
           "n_pages, page_rows and max_pages must be >= 1");
   REQUIRE((int64_t)kv->page_rows * kv->max_pages <= INT32_MAX, "page_rows * max_pages too large");
   REQUIRE_PTR(kv->pages);
   REQUIRE_PTR(kv->page_table);
   if (kv->fmt == CSA_MIXED_FP8_BF16) REQUIRE_PTR(kv->scales);
-  *out = KvLayout{kv->fmt == CSA_MIXED_FP8_BF16, kv->pages,
+  *out = KvLayout{kv->fmt == CSA_MIXED_FP8_BF16, kv->fmt == CSA_MIXED_MXFP4_BF16, kv->pages,
                   static_cast<const float*>(kv->scales), kv->page_table, kv->n_pages,
                   kv->page_rows, kv->max_pages};
   *N_cap = (int64_t)kv->page_rows * kv->max_pages;
@@ -875,7 +921,7 @@ csa_status csa_sparse_mqa_mixed_kv(const csa_params* p, int32_t B, int32_t T, co
                                    size_t ws_bytes, void* stream) {
   TRY(check_params(p));
   TRY(check_topk(p));
-  const KvLayout kv{true, kv_rows, kv_scale, nullptr, 0, 0, 0};
+  const KvLayout kv{true, false, kv_rows, kv_scale, nullptr, 0, 0, 0};
   return tc_mqa_ext("sparse MQA (mixed KV)", p, B, T, q, q_pos, kv, N_cap, idx, p->topk, win_kv,
                     L_raw, win_pos0, sink, q_rms_w, out, ws, ws_bytes, stream);
 }
@@ -887,7 +933,7 @@ csa_status hca_dense_mqa_mixed_kv(const csa_params* p, int32_t B, int32_t T, con
                                   const void* q_rms_w, void* out, void* ws, size_t ws_bytes,
                                   void* stream) {
   TRY(check_params(p));
-  const KvLayout kv{true, kv_rows, kv_scale, nullptr, 0, 0, 0};
+  const KvLayout kv{true, false, kv_rows, kv_scale, nullptr, 0, 0, 0};
   return tc_mqa_ext("dense MQA (mixed KV)", p, B, T, q, q_pos, kv, N_cap, nullptr, 0, win_kv,
                     L_raw, win_pos0, sink, q_rms_w, out, ws, ws_bytes, stream);
 }
@@ -1003,6 +1049,10 @@ csa_status csa_forward_paged(const csa_params* p, int32_t B, int32_t T, const cs
                      win_pos0, sink, q_rms_w, out);
   const bool rope_ok = !lay.mixed ||
                        (p->rope_dims > 0 && p->rope_dims < p->c && p->rope_dims % 16 == 0);
+  if (lay.fp4 && !csa::attn_fp4_supported(ma))
+    return fail(CSA_ERR_UNSUPPORTED,
+                "csa_forward_paged: 4-bit rows need c = 512, rope_dims = 64 and n_heads a "
+                "multiple of 64");
   if (!rope_ok || !csa::mqa_tc_supported(ma, true))
     return fail(CSA_ERR_UNSUPPORTED,
                 "csa_forward_paged: needs the tensor-core attention (c = 512, n_heads a multiple "
@@ -1017,18 +1067,16 @@ csa_status csa_forward_paged(const csa_params* p, int32_t B, int32_t T, const cs
   const size_t tb = round_up(csa::topk_workspace_bytes(B, T, N_cap, p->topk));
   void* sc = out_scores ? out_scores : base;
   ma.kv_scale = lay.mixed ? lay.scales : nullptr;
-  ma.page_table = lay.page_table;
-  ma.n_pages = lay.n_pages;
-  ma.page_rows = lay.page_rows;
-  ma.max_pages = lay.max_pages;
+  set_pages(&ma, lay);
+  ma.fp4 = lay.fp4;
   ma.chained = csa::topk_decode_path(B, T, N_cap, p->topk);  // as in csa_forward
-  const size_t mb = round_up(csa::mqa_workspace_bytes(ma));
+  const size_t mb = round_up(attn_bytes(ma, lay.fp4));
   csa::TopkArgs t{};
   t.B = B; t.T = T; t.m = p->m; t.k = p->topk; t.n_cap = N_cap; t.q_pos = q_pos;
   t.out_idx = out_idx;
   if (bf16_scores) t.scores16 = sc;
   else t.scores = static_cast<float*>(sc);
-  if (forward_qhat(p, B, T, N_cap)) {
+  if (!lay.fp4 && forward_qhat(p, B, T, N_cap)) {  // 4-bit rows: f16 q_hat, made by the attention
     t.qj.q = q;
     t.qj.q_rms_w = q_rms_w;
     t.qj.qhat = base + sb + tb + mb;
@@ -1043,7 +1091,9 @@ csa_status csa_forward_paged(const csa_params* p, int32_t B, int32_t T, const cs
   TRY(index_then_topk(p, keys->fmt, B, T, N_cap, qI, qI_scale, w, keys->pages, keys->scales,
                       q_pos, bf16_scores ? nullptr : static_cast<float*>(sc), t, base + sb, tb,
                       st, bf16_scores ? sc : nullptr, keys));
-  TRY(cuda_status(csa::launch_mqa(ma, true, base + sb + tb, mb, st), "sparse MQA (paged)"));
+  TRY(cuda_status(lay.fp4 ? csa::launch_attn_fp4(ma, base + sb + tb, mb, st)
+                          : csa::launch_mqa(ma, true, base + sb + tb, mb, st),
+                  "sparse MQA (paged)"));
   return ok();
 }
 

@@ -1,0 +1,542 @@
+// Stage 4 over 4-bit cache rows (CSA_MIXED_MXFP4_BF16 pages): shared-KV MQA, sparse CSA rows or
+// dense HCA rows, plus the sliding window, with query RMSNorm / RoPE, sink and output
+// un-rotation.
+//
+// 【论文解读】DeepSeek-V4 一(三)1(3) / 2(2): every KV row is key and value for all heads; 3(1)
+// RMSNorm of each query head; 3(2) RoPE(t) on the last r dims of q, RoPE(-t) on the output;
+// 3(3) window rows attended with the compressed rows; 3(4) exp(z'_h) in the denominator. The
+// row format is MXFP4 (OCP MX v1.0) for the values without RoPE, as 二(四) keeps the indexer's
+// keys, and bf16 for the RoPE values.
+//
+// Work: a stream is (query, group of 64 heads); its row list is cut into chunks of 64 rows
+// and split over `nsplit` CTAs. Per chunk, with f16 operands in 128B-swizzled shared memory
+// and fp32 accumulators in TMEM:
+//   S[64 heads x 64 rows] = q_hat . K^T          (M = 64; A = q_hat, B = the KV tile)
+//   P = 2^(S * scale * log2(e) - m_h) in f16     (two threads a head)
+//   O^T[4 x 128 dims x 64 heads] += V^T . P^T    (A = the same KV tile read MN-major)
+// Warps: 0-3 prepare q_hat, then softmax and epilogue; 4 issues the MMAs; 5 resolves
+// addresses; 6-13 each widen one 64-value atom of every row (kv_rows.cuh). Two KV buffers:
+// S of chunk j + 1 is issued before O^T of chunk j, so the tensor cores work during the
+// softmax, and the gather warps fill the buffer that O^T released.
+// The running max m_h is raised only when a chunk's max exceeds it by more than 2^11.5 (then
+// O^T and l are rescaled); P stays below 2^11.5, inside f16, and sums are fp32.
+// One split: the CTA finalises. Several: it writes (m, l, O) partials and k_attn_fp4_combine
+// merges them in a fixed order.
+#include <cmath>
+
+#include "common.cuh"
+#include "host_util.cuh"
+#include "internal.h"
+#include "kv_rows.cuh"
+#include "tc.cuh"
+
+namespace csa {
+
+namespace {
+
+using namespace tc;
+using namespace rows;
+
+constexpr int kThreads = 14 * 32;
+constexpr int kBuf = 2;
+constexpr float kLazy = 11.5f;  // rescale threshold (log2 units)
+constexpr int kMaxSplit = 32;
+
+constexpr int kSlotKV = kAtoms * kAtomBytes;  // 64 KB
+constexpr int kOffKV = 0;
+constexpr int kOffQ = kBuf * kSlotKV;         // [atom][head][128 B]
+constexpr int kOffP = kOffQ + kAtoms * kHg * 128;
+constexpr int kSlotP = kHg * 128;             // [head][64 rows]
+constexpr int kOffEnd = kOffP + kBuf * kSlotP;
+
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0;    // S: two tiles of 64 columns (M = 64 layout)
+constexpr uint32_t kColO = 256;  // O^T slice s: 256 + 64 s
+
+// 211 ring free, 212 ring full / 213 buffer free, 214 KV / q_hat / P full, 215 S / O^T done;
+// 216 = 211 + 5: a page id outside the pool
+enum { kErrRing = 211, kErrGather = 212, kErrMma = 214, kErrSoftmax = 215 };
+
+struct Smem {
+  AddrRing ring;
+  uint64_t kv_full[kBuf * kAtoms], kv_free[kBuf], s_full[kBuf], p_full[kBuf], q_full, done;
+  uint32_t tmem_slot;
+  float m_used[kHg], l_sum[kHg], alpha[kHg], fin[kHg];
+  RopeTable rope;
+};
+
+struct Params {
+  MqaArgs a;
+  int G, nsplit;
+  float* part;  // [stream][split][64 m | 64 l | 64 x 512 O], or nullptr
+  float scale2; // scale * log2(e)
+  double inv_freq[kR / 2];
+};
+
+constexpr size_t kPartFloats = (size_t)kHg * (kC + 2);
+
+__device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool reduce_softmax(bool p, bool all) {
+  uint32_t res;
+  if (all)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.and.pred p, 1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(res) : "r"((uint32_t)p) : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.or.pred p, 1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(res) : "r"((uint32_t)p) : "memory");
+  return res != 0;
+}
+
+// 16 TMEM lanes x 64 columns, two threads per lane: thread t of the warp gets lane
+// t / 4 + 8 (t % 2) and, in register i, column 2 i + (t / 2) % 2.
+__device__ __forceinline__ void tmem_ld_16x64b_x32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x64b.x32.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
+      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31},"
+      " [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
+      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant__ Params P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = smem_align1024(smem_raw);
+  Smem& S = *reinterpret_cast<Smem*>(base + kOffEnd);
+  const MqaArgs& a = P.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int stream = blockIdx.x / P.nsplit, split = blockIdx.x % P.nsplit;
+  const int bt = stream / P.G, g = stream % P.G, b = bt / a.T, h0 = g * kHg;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      for (int i = 0; i < kRing; ++i) {
+        mbar_init(&S.ring.full[i], 1);
+        mbar_init(&S.ring.free[i], 8 + 4);  // gather warps; softmax warps (the mask)
+      }
+      for (int i = 0; i < kBuf * kAtoms; ++i) mbar_init(&S.kv_full[i], 1);
+      for (int i = 0; i < kBuf; ++i) {
+        mbar_init(&S.kv_free[i], 1);
+        mbar_init(&S.s_full[i], 1);
+        mbar_init(&S.p_full[i], 4);
+      }
+      mbar_init(&S.q_full, 4);
+      mbar_init(&S.done, 1);
+      fence_barrier_init();
+    }
+    __syncwarp();
+    tmem_alloc(&S.tmem_slot, kTmemCols);
+  }
+  pdl_wait();  // positions, lists and queries may belong to the previous kernels
+  const List l = make_list(a, bt);
+  const int c0 = (int)(((int64_t)l.n_chunks * split) / P.nsplit);
+  const int c1 = (int)(((int64_t)l.n_chunks * (split + 1)) / P.nsplit);
+  if (warp == 0) rope_angle_cs((double)l.t, P.inv_freq[lane], &S.rope.cs[lane], &S.rope.sn[lane]);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();
+  const uint32_t tmem = S.tmem_slot;
+
+  if (warp >= 6) {
+    gather_loop<kFp4>(base + kOffKV, kBuf, c0, c1, l.nc, warp - 6, S.ring, S.kv_full, S.kv_free,
+                      kErrGather);
+  } else if (warp == 5) {
+    resolve_rows<kFp4>(a, l, bt, b, c0, c1, S.ring, kErrRing);
+  } else if (warp == 4) {
+    // ------------------------------ MMA issuer ------------------------------
+    const uint32_t idS = idesc_f16(0, kHg, kRows);             // M = 64, N = 64, both K-major
+    const uint32_t idO = idesc_f16(0, 128, kHg) | (1u << 15);  // M = 128 dims; A MN-major
+    const uint64_t dq = smem_desc(smem_u32(base + kOffQ), 16, 1024, kLayoutSw128);
+    bool ok = c0 < c1 && __all_sync(0xffffffffu, mbar_wait(&S.q_full, 0, kErrMma));
+    auto issue_s = [&](int j) {
+      const int it = j - c0, slot = it % kBuf;
+      const uint32_t ph = (uint32_t)(it / kBuf) & 1;
+      const uint64_t dk = smem_desc(smem_u32(base + kOffKV + slot * kSlotKV), 16, 1024, kLayoutSw128);
+#pragma unroll
+      for (int atom = 0; atom < kAtoms; ++atom) {
+        ok = ok && __all_sync(0xffffffffu,
+                              mbar_wait(&S.kv_full[slot * kAtoms + atom], ph, kErrMma));
+        if (!ok) return;
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int kq = 0; kq < 4; ++kq)
+            mma_f16(tmem + kColS + 64 * slot, dq + ((atom * (kHg * 128) + kq * 32) >> 4),
+                    dk + ((atom * kAtomBytes + kq * 32) >> 4), idS, (atom | kq) != 0 ? 1u : 0u);
+        }
+      }
+      if (lane == 0) mma_commit(&S.s_full[slot]);
+      __syncwarp();
+    };
+    if (ok) issue_s(c0);
+    for (int j = c0; j < c1 && ok; ++j) {
+      const int it = j - c0, slot = it % kBuf;
+      if (j + 1 < c1) {
+        // S tile (j + 1) % 2 was read by the softmax of chunk j - 1 before it published P(j - 1),
+        // which this warp has waited for
+        issue_s(j + 1);
+        if (!ok) break;
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(&S.p_full[slot], (uint32_t)(it / kBuf) & 1, kErrMma));
+      if (!ok) break;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint64_t dv = smem_desc(smem_u32(base + kOffKV + slot * kSlotKV), kAtomBytes, 1024,
+                                      kLayoutSw128);
+        const uint64_t dp = smem_desc(smem_u32(base + kOffP + slot * kSlotP), 16, 1024, kLayoutSw128);
+#pragma unroll
+        for (int kk = 0; kk < kRows / 16; ++kk)
+#pragma unroll
+          for (int sl = 0; sl < 4; ++sl)
+            mma_f16(tmem + kColO + 64 * sl, dv + ((sl * 2 * kAtomBytes + kk * 2048) >> 4),
+                    dp + ((kk * 32) >> 4), idO, (j > c0 || kk > 0) ? 1u : 0u);
+        mma_commit(&S.kv_free[slot]);
+      }
+      __syncwarp();
+    }
+    if (lane == 0) {  // nothing this thread issued is in flight once `done` fires
+      mma_commit(&S.done);
+      mbar_wait(&S.done, 0, kErrMma);
+    }
+    __syncwarp();
+  } else {
+    // ---- q_hat: a warp per head, eight heads in flight ----
+    {
+      float w[16];
+      qhat_weights(a.q_rms_w, w);
+      const uint4* qg = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                       ((size_t)bt * a.H + h0) * kC);
+      uint8_t* qs = base + kOffQ;
+#pragma unroll 1
+      for (int hb = 0; hb < 16; hb += 8) {
+        uint4 raw[8][2];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+            raw[i][half] = __ldg(qg + (size_t)(16 * warp + hb + i) * (kC / 8) + 32 * half + lane);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int h = 16 * warp + hb + i;
+          float y[16];
+          qhat_lane(raw[i], w, a.eps, S.rope, y);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              o[k] = pack2<kFp4>(y[8 * half + 2 * k], y[8 * half + 2 * k + 1]);
+            const int c = lane + 32 * half;  // 16-byte piece of the row
+            *reinterpret_cast<uint4*>(qs + (c >> 3) * (kHg * 128) + sw128(h, c & 7)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.q_full);
+    }
+    // ------------------------------ softmax ------------------------------
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * warp) << 16);
+    // the M = 64 accumulator puts head 16w + i in TMEM lane 32w + i (i < 16); threads t and
+    // t ^ 2 share head 16w + t / 4 + 8 (t % 2), each with every other row of a chunk
+    const int par = (lane >> 1) & 1;
+    const int hh = 16 * warp + (lane >> 2) + 8 * (lane & 1);
+    float mu = -INFINITY, lsum = 0.f;
+    bool ok = true;
+#pragma unroll 1
+    for (int j = c0; j < c1 && ok; ++j) {
+      const int it = j - c0, slot = it % kBuf, rs = it % kRing;
+      ok = reduce_softmax(mbar_wait(&S.s_full[slot], (uint32_t)(it / kBuf) & 1, kErrSoftmax), true);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t sv[32];
+      tmem_ld_16x64b_x32(lane_base + kColS + 64 * slot, sv);
+      tmem_ld_wait();
+      const uint32_t vm[2] = {S.ring.mask[rs][0], S.ring.mask[rs][1]};
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.ring.free[rs]);
+      float cmx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const int rr = 2 * i + par;
+        const float x =
+            ((vm[rr >> 5] >> (rr & 31)) & 1u) ? __uint_as_float(sv[i]) * P.scale2 : -INFINITY;
+        sv[i] = __float_as_uint(x);
+        cmx[i & 3] = fmaxf(cmx[i & 3], x);
+      }
+      float cm = fmaxf(fmaxf(cmx[0], cmx[1]), fmaxf(cmx[2], cmx[3]));
+      cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 2));
+      float al = 1.f;
+      if (cm > mu + kLazy || (mu == -INFINITY && cm != -INFINITY)) {
+        al = mu == -INFINITY ? 0.f : exp2f(mu - cm);
+        mu = cm;
+      }
+      lsum *= al;
+      if (par == 0) S.alpha[hh] = al;
+      if (reduce_softmax(al != 1.f && j > c0, false)) {
+        // rare: scale O^T by alpha once the previous chunk's products are done
+        const int pi = it - 1;
+        ok = reduce_softmax(mbar_wait(&S.kv_free[pi % kBuf], (uint32_t)(pi / kBuf) & 1, kErrSoftmax),
+                            true);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int cg = 0; cg < 16; ++cg) {  // 4 slices x 4 groups of 16 heads
+          uint32_t o[16];
+          const uint32_t ta = lane_base + kColO + 16 * cg;
+          tmem_ld_x16(ta, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int h = 0; h < 16; ++h)
+            o[h] = __float_as_uint(__uint_as_float(o[h]) * S.alpha[16 * (cg & 3) + h]);
+          tmem_st_x16(ta, o);
+        }
+        tmem_st_wait();
+      }
+      // the P buffer was read by the products of chunk j - 2
+      if (it >= kBuf) {
+        const int pi = it - kBuf;
+        ok = reduce_softmax(mbar_wait(&S.kv_free[slot], (uint32_t)(pi / kBuf) & 1, kErrSoftmax), true);
+        if (!ok) break;
+      }
+      // P row of this head into the K-major tile [head][64 rows]. Per 16 rows the even thread
+      // writes rows 0-7 and the odd one rows 8-15, after exchanging four values.
+      {
+        uint8_t* pt = base + kOffP + slot * kSlotP;
+        float lc[4] = {0.f, 0.f, 0.f, 0.f};  // sums of what the MMA multiplies
+        const float mref = mu == -INFINITY ? 0.f : mu;
+#pragma unroll
+        for (int gr = 0; gr < kRows / 16; ++gr) {
+          uint32_t bb[8];
+#pragma unroll
+          for (int m = 0; m < 8; ++m) {
+            const __half hv = __float2half_rn(exp2f(__uint_as_float(sv[8 * gr + m]) - mref));
+            lc[m & 3] += __half2float(hv);
+            bb[m] = (uint32_t)__half_as_ushort(hv);
+          }
+          const uint32_t s0 = par ? (bb[0] | (bb[1] << 16)) : (bb[4] | (bb[5] << 16));
+          const uint32_t s1 = par ? (bb[2] | (bb[3] << 16)) : (bb[6] | (bb[7] << 16));
+          const uint32_t r0 = __shfl_xor_sync(0xffffffffu, s0, 2);
+          const uint32_t r1 = __shfl_xor_sync(0xffffffffu, s1, 2);
+          const uint32_t pk[4] = {r0 & 0xffffu, r0 >> 16, r1 & 0xffffu, r1 >> 16};
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t own = par ? bb[4 + k] : bb[k];
+            w[k] = par ? (pk[k] | (own << 16)) : (own | (pk[k] << 16));
+          }
+          *reinterpret_cast<uint4*>(pt + sw128(hh, 2 * gr + par)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        lsum += (lc[0] + lc[1]) + (lc[2] + lc[3]);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.p_full[slot]);
+    }
+    lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
+    if (par == 0) {
+      S.m_used[hh] = mu;
+      S.l_sum[hh] = lsum;
+    }
+    // ---- epilogue ----
+    if (ok && c1 > c0) {
+      const int last = c1 - c0 - 1;
+      ok = reduce_softmax(
+          mbar_wait(&S.kv_free[last % kBuf], (uint32_t)(last / kBuf) & 1, kErrSoftmax), true);
+    }
+    bar_softmax();
+    const bool single = P.nsplit == 1;
+    float* pp = single ? nullptr : P.part + ((size_t)stream * P.nsplit + split) * kPartFloats;
+    if (tid < kHg) {
+      const float m = S.m_used[tid], lv = S.l_sum[tid];
+      if (single) {
+        const float zs = a.sink ? a.sink[h0 + tid] * 1.44269504088896341f : -INFINITY;
+        float f = 0.f;
+        if (lv > 0.f) {
+          const float M = fmaxf(m, zs);
+          const float e = exp2f(m - M);
+          f = e / (lv * e + (zs == -INFINITY ? 0.f : exp2f(zs - M)));
+        }
+        S.fin[tid] = f;
+      } else {
+        pp[tid] = m;
+        pp[kHg + tid] = lv;
+      }
+    }
+    bar_softmax();
+    tc_fence_after();
+    const bool have = ok && c1 > c0;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((size_t)bt * a.H + h0) * kC;
+    // O^T slice by slice: thread = dim 128 sl + tid, 64 heads
+#pragma unroll 1
+    for (int sl = 0; sl < 4; ++sl) {
+      uint32_t o[64];
+      if (have) {
+        tmem_ld_32x32b_x64(lane_base + kColO + 64 * sl, o);
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int h = 0; h < 64; ++h) o[h] = 0u;
+      }
+      const int d = 128 * sl + tid;
+      if (single) {
+        float cs = 1.f, sn = 0.f;
+        const bool rot = d >= kNope;
+        if (rot) {
+          cs = S.rope.cs[(d - kNope) >> 1];
+          sn = -S.rope.sn[(d - kNope) >> 1];  // rotation by -t
+        }
+#pragma unroll
+        for (int h = 0; h < 64; ++h) {
+          const float y = __uint_as_float(o[h]) * S.fin[h];
+          const float yp = __shfl_xor_sync(0xffffffffu, y, 1);
+          float z = y;
+          if (rot) z = (d & 1) == 0 ? y * cs - yp * sn : yp * sn + y * cs;
+          out[(size_t)h * kC + d] = __float2bfloat16_rn(z);
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 64; ++h) pp[2 * kHg + (size_t)h * kC + d] = __uint_as_float(o[h]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Merge the partials of one head (fixed split order), add the sink, rotate by -t.
+__global__ void __launch_bounds__(256) k_attn_fp4_combine(const __grid_constant__ Params P) {
+  pdl_wait();
+  pdl_trigger();
+  const MqaArgs& a = P.a;
+  const int stream = blockIdx.x, h = blockIdx.y;
+  const int bt = stream / P.G, g = stream % P.G;
+  const int64_t t = a.q_pos[bt];
+  const int d = 2 * threadIdx.x, ns = P.nsplit;
+  const float* base = P.part + (size_t)stream * ns * kPartFloats;
+  float ms[kMaxSplit], M = -INFINITY;
+#pragma unroll
+  for (int s = 0; s < kMaxSplit; ++s) {
+    ms[s] = s < ns ? base[s * kPartFloats + h] : -INFINITY;
+    M = fmaxf(M, ms[s]);
+  }
+  const float zs = a.sink ? a.sink[g * kHg + h] * 1.44269504088896341f : -INFINITY;
+  M = fmaxf(M, zs);
+  float l = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll
+  for (int s = 0; s < kMaxSplit; ++s) {
+    if (ms[s] != -INFINITY) {
+      const float f = exp2f(ms[s] - M);
+      const float* pp = base + s * kPartFloats;
+      l = fmaf(pp[kHg + h], f, l);
+      const float2 o = *reinterpret_cast<const float2*>(pp + 2 * kHg + (size_t)h * kC + d);
+      o0 = fmaf(o.x, f, o0);
+      o1 = fmaf(o.y, f, o1);
+    }
+  }
+  float y0 = 0.f, y1 = 0.f;
+  if (l > 0.f) {
+    const float den = l + (zs == -INFINITY ? 0.f : exp2f(zs - M));
+    y0 = o0 / den;
+    y1 = o1 / den;
+  }
+  if (d >= kNope) {
+    float cs, sn;
+    rope_angle_cs(-(double)t, P.inv_freq[(d - kNope) >> 1], &cs, &sn);
+    const float u0 = y0 * cs - y1 * sn, u1 = y0 * sn + y1 * cs;
+    y0 = u0;
+    y1 = u1;
+  }
+  __nv_bfloat16* out =
+      static_cast<__nv_bfloat16*>(a.out) + ((size_t)bt * a.H + g * kHg + h) * kC + d;
+  *reinterpret_cast<__nv_bfloat162*>(out) = __floats2bfloat162_rn(y0, y1);
+}
+
+// CTAs per stream: as many as fill the SMs, at most one per chunk of the longest list, at
+// most kMaxSplit.
+int choose_split(const MqaArgs& a) {
+  const int64_t streams = (int64_t)a.B * a.T * (a.H / kHg);
+  const int64_t rows = a.k > 0 ? a.k : a.n_cap;
+  const int64_t chunks = (rows + kRows - 1) / kRows + ((int64_t)a.n_win + kRows - 1) / kRows;
+  int64_t ns = device_sm_count() / (streams > 0 ? streams : 1);
+  ns = ns < chunks ? ns : chunks;
+  return (int)(ns < 1 ? 1 : (ns > kMaxSplit ? kMaxSplit : ns));
+}
+
+}  // namespace
+
+bool attn_fp4_supported(const MqaArgs& a) {
+  return a.c == kC && a.rope_dims == kR && a.H >= kHg && a.H % kHg == 0;
+}
+
+size_t attn_fp4_workspace_bytes(const MqaArgs& a) {
+  const int ns = choose_split(a);
+  if (ns <= 1) return 0;
+  return (size_t)a.B * a.T * (a.H / kHg) * ns * kPartFloats * sizeof(float);
+}
+
+cudaError_t launch_attn_fp4(const MqaArgs& a, void* ws, size_t ws_bytes, cudaStream_t st) {
+  Params P;
+  P.a = a;
+  P.G = a.H / kHg;
+  P.nsplit = choose_split(a);
+  P.part = P.nsplit > 1 ? static_cast<float*>(ws) : nullptr;
+  P.scale2 = a.scale * 1.44269504088896341f;
+  for (int p = 0; p < kR / 2; ++p) P.inv_freq[p] = rope_inv_freq(p, kR, (double)a.rope_base);
+  if (P.nsplit > 1 && ws_bytes < attn_fp4_workspace_bytes(a)) return cudaErrorInvalidValue;
+  const int64_t streams = (int64_t)a.B * a.T * P.G;
+  const size_t smem = 1024 + kOffEnd + sizeof(Smem);
+  cudaError_t e = cudaFuncSetAttribute(k_attn_fp4, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem);
+  if (e != cudaSuccess) return e;
+  e = launch(a.chained, k_attn_fp4, dim3((unsigned)(streams * P.nsplit)), dim3(kThreads), smem, st,
+             P);
+  if (e != cudaSuccess || P.nsplit == 1) return e;
+  return launch(true, k_attn_fp4_combine, dim3((unsigned)streams, kHg), dim3(256), 0, st, P);
+}
+
+cudaError_t attn_fp4_device_error(int* code) {
+  int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(code, tc::g_device_error, sizeof(int));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(tc::g_device_error, &zero, sizeof(int));
+}
+
+}  // namespace csa

@@ -160,6 +160,7 @@ struct MqaArgs {
                               // page page_table[b * max_pages + e / page_rows];
                               // n_cap = page_rows * max_pages
   int page_rows, max_pages, n_pages;
+  bool fp4;  // `kv` is a pool of 4-bit rows (CSA_MIXED_MXFP4_BF16) read by attn_fp4.cu
 };
 size_t mqa_workspace_bytes(const MqaArgs& a);
 // tensor-core attention (bf16, c = 512, heads in groups of 64)
@@ -170,6 +171,11 @@ size_t mqa_tc_workspace_bytes(const MqaArgs& a);
 cudaError_t launch_zero(void* p0, size_t b0, void* p1, size_t b1, cudaStream_t st);
 cudaError_t launch_mqa_tc(const MqaArgs& a, void* ws, size_t ws_bytes, cudaStream_t st);
 cudaError_t mqa_tc_device_error(int* code);
+// attention over 4-bit cache rows (c = 512, 64 RoPE dims, heads in groups of 64)
+bool attn_fp4_supported(const MqaArgs& a);
+size_t attn_fp4_workspace_bytes(const MqaArgs& a);
+cudaError_t launch_attn_fp4(const MqaArgs& a, void* ws, size_t ws_bytes, cudaStream_t st);
+cudaError_t attn_fp4_device_error(int* code);
 cudaError_t launch_mqa(const MqaArgs& a, bool bf16, void* ws, size_t ws_bytes, cudaStream_t st);
 
 // Records a formatted message as the calling thread's csa_last_error() and returns `s`.

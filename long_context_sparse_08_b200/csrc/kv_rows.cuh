@@ -1,0 +1,337 @@
+// Building blocks of the kernels that stream a query's KV rows through the tensor cores in
+// chunks of 64 rows (attn_fp4.cu, attn_mass.cu): the row list of a query, the warp that
+// resolves a chunk's rows to addresses, the eight warps that bring one 64-value atom of every
+// row each into 128B-swizzled shared memory (widening 4-bit rows on the way), and the warps
+// that prepare q_hat.
+//
+// A 4-bit cache row (CSA_MIXED_MXFP4_BF16, c = 512, r = 64) is 368 bytes:
+//   bytes   0-223  448 e2m1 codes, element 2j in the low nibble of byte j
+//   bytes 224-239  14 e8m0 exponents (one per 32 values), then 2 zero bytes
+//   bytes 240-367  the 64 RoPE values, bf16
+// Its operands are f16. An e2m1 value times 2^E with E in [-14, 13] (the writers clamp E to
+// that range) is an f16 number, and so is every bf16 value of magnitude 2^-14 .. 65504, so
+// widening a row rounds nothing (smaller RoPE or window values keep an absolute step of
+// 2^-24); q_hat and P carry 11 bits where bf16 operands would carry 8.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "tc.cuh"
+
+namespace csa {
+namespace rows {
+
+using namespace tc;
+
+constexpr int kC = 512, kR = 64, kNope = kC - kR;
+constexpr int kHg = 64;            // heads of a CTA
+constexpr int kRows = 64;          // rows of a chunk
+constexpr int kAtoms = kC / 64;    // 64-value (128 B) atoms of a row
+constexpr int kAtomBytes = kRows * 128;
+constexpr int kFp4RowBytes = 368, kFp4Exps = 224, kFp4Rope = 240;
+constexpr int kRing = 4;           // chunks of resolved addresses
+constexpr int32_t kEvictedPage = -2;
+
+enum Fmt { kFp4 = 0, kBf16 = 1 };
+
+__device__ __forceinline__ uint32_t sw128(uint32_t row, uint32_t chunk) {
+  return row * 128u + ((chunk ^ (row & 7u)) << 4);
+}
+
+// The rows of a query: cache chunks (selected or visible entries), then window chunks. Each
+// kind starts a chunk of its own, so every row of a chunk has one storage format.
+struct List {
+  int64_t t, lo;
+  int n_vis, n_sel, n_w, nc, n_chunks;
+};
+
+__device__ __forceinline__ List make_list(const MqaArgs& a, int bt) {
+  List l;
+  l.t = a.q_pos[bt];
+  l.n_vis = l.t < 0 ? 0 : (int)(l.t / a.m < a.n_cap ? l.t / a.m : a.n_cap);
+  l.n_sel = a.k > 0 ? a.k : l.n_vis;
+  l.lo = (l.t - a.n_win + 1) > 0 ? (l.t - a.n_win + 1) : 0;
+  l.n_w = (a.n_win > 0 && l.t >= 0) ? (int)(l.t - l.lo + 1) : 0;
+  l.nc = (l.n_sel + kRows - 1) / kRows;
+  l.n_chunks = l.nc + (l.n_w + kRows - 1) / kRows;
+  return l;
+}
+
+// Resolved addresses of kRing chunks (0: masked row) and their masks of valid rows.
+struct AddrRing {
+  uint64_t src[kRing][kRows];
+  uint32_t mask[kRing][2];
+  uint64_t full[kRing], free[kRing];
+};
+
+// The address warp: chunks [c0, c1) of the list, four at a time, so that four chunks share
+// the two dependent round trips (index list, page table). `code`: error code of a
+// wait that gave up; code + 5: a page id outside the pool (an evicted page is masked quietly).
+template <int kFmt>
+__device__ __forceinline__ void resolve_rows(const MqaArgs& a, const List& l, int bt, int b,
+                                             int c0, int c1, AddrRing& ring, int code) {
+  const int lane = threadIdx.x & 31;
+  const size_t row_bytes = kFmt == kFp4 ? kFp4RowBytes : kC * 2;
+  for (int j0 = c0; j0 < c1; j0 += kRing) {
+    int e[kRing][2];
+    int32_t pg[kRing][2];
+#pragma unroll
+    for (int i = 0; i < kRing; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int s = (j0 + i) * kRows + 32 * h + lane;
+        e[i][h] = -1;
+        if (j0 + i < c1 && j0 + i < l.nc && s < l.n_sel)
+          e[i][h] = a.k > 0 ? a.idx[(size_t)bt * a.k + s] : s;
+      }
+#pragma unroll
+    for (int i = 0; i < kRing; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        pg[i][h] = kEvictedPage;
+        if (e[i][h] >= 0 && e[i][h] < a.n_cap)
+          pg[i][h] = a.page_table[(size_t)b * a.max_pages + (uint32_t)e[i][h] / (uint32_t)a.page_rows];
+      }
+#pragma unroll
+    for (int i = 0; i < kRing; ++i) {
+      const int j = j0 + i;
+      if (j >= c1) break;
+      uint64_t src[2] = {0, 0};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (j < l.nc) {
+          const int32_t p = pg[i][h];
+          if (p >= 0 && p < a.n_pages) {
+            const size_t row = (size_t)p * a.page_rows + (uint32_t)e[i][h] % (uint32_t)a.page_rows;
+            src[h] = reinterpret_cast<uint64_t>(a.kv) + row * row_bytes;
+          } else if (p != kEvictedPage) {
+            set_error(code + 5);
+          }
+        } else {
+          const int s = (j - l.nc) * kRows + 32 * h + lane;
+          if (s < l.n_w) {
+            const int64_t pos = l.lo + s;
+            // win_pos0 == nullptr: the state cache's ring (position p in row p mod l_raw)
+            const int64_t rr = a.win_pos0 != nullptr ? pos - a.win_pos0[b] : pos % a.l_raw;
+            if (rr >= 0 && rr < a.l_raw)
+              src[h] = reinterpret_cast<uint64_t>(a.win) + ((size_t)b * a.l_raw + rr) * (kC * 2);
+          }
+        }
+      }
+      const int it = j - c0;
+      if (!__all_sync(0xffffffffu, mbar_wait(&ring.free[it % kRing],
+                                             ((uint32_t)(it / kRing) & 1) ^ 1, code)))
+        return;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        ring.src[it % kRing][32 * h + lane] = src[h];
+        const uint32_t m = __ballot_sync(0xffffffffu, src[h] != 0);
+        if (lane == 0) ring.mask[it % kRing][h] = m;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ring.full[it % kRing]);
+    }
+  }
+}
+
+// Eight e2m1 codes (a 32-bit word, element 0 in the low nibble) times the f16x2 scale.
+__device__ __forceinline__ uint4 widen8(uint32_t w, __half2 scale) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h[i]), scale);
+    h[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+// 2^E of an exponent byte as f16x2, E clamped to the format's [-14, 13].
+__device__ __forceinline__ __half2 scale_h2(uint32_t ex) {
+  const uint32_t s = min(max(ex, 113u), 140u) - 112u;  // E + 15
+  const uint32_t u = (s << 10) | (s << 26);
+  return *reinterpret_cast<const __half2*>(&u);
+}
+
+// Two bf16 values to f16 (exact for magnitudes 2^-14 .. 65504; larger ones become infinite).
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
+  const __half2 h = __floats2half2_rn(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// One gather warp's share of a chunk, its atom (64 values) of all 64 rows, held in registers
+// between the loads and the stores, so that the loads are in flight while the warp waits for
+// the buffer. Codes: lane -> 16-byte unit lane % 2 (one exponent block) of rows
+// lane / 2 + 16 i, four units a lane; the four 16-byte stores of eight neighbouring lanes
+// fall into distinct banks. bf16 values: unit lane % 8 of rows lane / 8 + 4 i, sixteen a lane.
+struct Held {
+  uint4 raw[16];
+  uint32_t ex[4];
+};
+
+template <int kFmt>
+__device__ __forceinline__ bool holds_codes(bool cache, int atom) {
+  return kFmt == kFp4 && cache && atom < kAtoms - 1;
+}
+
+template <int kFmt>
+__device__ __forceinline__ void load_atom(Held& v, const uint64_t* src, bool cache, int atom) {
+  const int lane = threadIdx.x & 31;
+  if (holds_codes<kFmt>(cache, atom)) {
+    const int u = lane & 1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint8_t* p = reinterpret_cast<const uint8_t*>(src[(lane >> 1) + 16 * i]);
+      v.raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      v.ex[i] = 127;
+      if (p != nullptr) {
+        v.raw[i] = __ldg(reinterpret_cast<const uint4*>(p + 32 * atom + 16 * u));
+        v.ex[i] = __ldg(p + kFp4Exps + 2 * atom + u);
+      }
+    }
+  } else {
+    const int off = (kFmt == kFp4 && cache ? kFp4Rope : 128 * atom) + 16 * (lane & 7);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint8_t* p = reinterpret_cast<const uint8_t*>(src[(lane >> 3) + 4 * i]);
+      v.raw[i] = p != nullptr ? __ldg(reinterpret_cast<const uint4*>(p + off))
+                              : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+}
+
+template <int kFmt>
+__device__ __forceinline__ void store_atom(const Held& v, uint8_t* dst, bool cache, int atom) {
+  const int lane = threadIdx.x & 31;
+  if (holds_codes<kFmt>(cache, atom)) {
+    const int u = lane & 1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = (lane >> 1) + 16 * i;
+      const __half2 s = scale_h2(v.ex[i]);
+      const uint32_t w[4] = {v.raw[i].x, v.raw[i].y, v.raw[i].z, v.raw[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint4*>(dst + sw128(row, 4 * u + k)) = widen8(w[k], s);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      uint4 o = v.raw[i];
+      if constexpr (kFmt == kFp4)
+        o = make_uint4(bf16x2_to_f16x2(o.x), bf16x2_to_f16x2(o.y), bf16x2_to_f16x2(o.z),
+                       bf16x2_to_f16x2(o.w));
+      *reinterpret_cast<uint4*>(dst + sw128((lane >> 3) + 4 * i, lane & 7)) = o;
+    }
+  }
+}
+
+// cos / sin of the query position for the 32 RoPE pairs.
+struct RopeTable {
+  float cs[kR / 2], sn[kR / 2];
+};
+
+// The 16 q_hat values of a lane (dims 8 lane .. and 256 + 8 lane ..) of one head, fp32:
+// RoPE_t(RMSNorm(q) * w). `raw`: the lane's two 16-byte pieces of the head's bf16 row.
+__device__ __forceinline__ void qhat_lane(const uint4 (&raw)[2], const float (&w)[16], float eps,
+                                          const RopeTable& rope, float (&y)[16]) {
+  const int lane = threadIdx.x & 31;
+  float ss = 0.f;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const uint32_t w4[4] = {raw[half].x, raw[half].y, raw[half].z, raw[half].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float lo = __uint_as_float(w4[k] << 16), hi = __uint_as_float(w4[k] & 0xffff0000u);
+      y[8 * half + 2 * k] = lo;
+      y[8 * half + 2 * k + 1] = hi;
+      ss = fmaf(lo, lo, ss);
+      ss = fmaf(hi, hi, ss);
+    }
+  }
+  const float rstd = 1.f / sqrtf(warp_sum(ss) / (float)kC + eps);
+#pragma unroll
+  for (int k = 0; k < 16; ++k) y[k] = y[k] * rstd * w[k];
+  if (lane >= 24) {  // dims 256 + 8 lane >= 448
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int p = 4 * (lane - 24) + k;
+      const float c = rope.cs[p], s = rope.sn[p], u = y[8 + 2 * k], v = y[9 + 2 * k];
+      y[8 + 2 * k] = u * c - v * s;
+      y[9 + 2 * k] = u * s + v * c;
+    }
+  }
+}
+
+__device__ __forceinline__ void qhat_weights(const void* q_rms_w, float (&w)[16]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int half = 0; half < 2; ++half)
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      w[8 * half + k] = q_rms_w ? __bfloat162float(static_cast<const __nv_bfloat16*>(
+                                      q_rms_w)[256 * half + 8 * lane + k])
+                                : 1.f;
+}
+
+// Eight fp32 values to 16-bit operands (f16 for 4-bit caches, else bf16).
+template <int kFmt>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (kFmt == kFp4) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+template <int kFmt>
+__device__ __forceinline__ float unpack_lo(uint32_t w) {
+  if constexpr (kFmt == kFp4) return __half2float(__ushort_as_half((unsigned short)(w & 0xffffu)));
+  else return __uint_as_float(w << 16);
+}
+template <int kFmt>
+__device__ __forceinline__ float unpack_hi(uint32_t w) {
+  if constexpr (kFmt == kFp4) return __half2float(__ushort_as_half((unsigned short)(w >> 16)));
+  else return __uint_as_float(w & 0xffff0000u);
+}
+
+// The gather warps' loop over chunks [c0, c1): `bufs` KV buffers of kAtoms atoms at `kv`, a
+// full barrier per (buffer, atom) and a free barrier per buffer. Loads of a chunk are issued
+// before the wait for its buffer.
+template <int kFmt>
+__device__ __forceinline__ void gather_loop(uint8_t* kv, int bufs, int c0, int c1, int nc,
+                                            int atom, AddrRing& ring, uint64_t* full,
+                                            uint64_t* free, int code) {
+  const int lane = threadIdx.x & 31;
+  Held v;
+  bool ok = true;
+  for (int j = c0; j < c1 && ok; ++j) {
+    const int it = j - c0, rs = it % kRing, slot = it % bufs;
+    ok = __all_sync(0xffffffffu, mbar_wait(&ring.full[rs], (uint32_t)(it / kRing) & 1, code));
+    if (!ok) break;
+    const bool cache = j < nc;
+    load_atom<kFmt>(v, ring.src[rs], cache, atom);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ring.free[rs]);
+    ok = __all_sync(0xffffffffu,
+                    mbar_wait(&free[slot], ((uint32_t)(it / bufs) & 1) ^ 1, code + 1));
+    if (!ok) break;
+    store_atom<kFmt>(v, kv + (size_t)(slot * kAtoms + atom) * kAtomBytes, cache, atom);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&full[slot * kAtoms + atom]);
+  }
+}
+
+}  // namespace rows
+}  // namespace csa

@@ -66,6 +66,30 @@ __device__ __forceinline__ void store_finished(const state::Args& a, const float
     if (threadIdx.x == 0) static_cast<float*>(a.page_scales)[prow] = scale;
     return;
   }
+  if (a.out == state::kOutMixedFp4) {
+    // a warp's 32 consecutive channels are one MX block, or RoPE values (c - r is a multiple
+    // of 32)
+    const int r0 = a.c - a.rope_dims;
+    uint8_t* rowp = static_cast<uint8_t*>(a.pages) + prow * state::fp4_row_bytes(a.c, a.rope_dims);
+    uint8_t* exps = rowp + state::fp4_exps_offset(a.c, a.rope_dims);
+    const size_t rope_off = state::fp4_rope_offset(a.c, a.rope_dims);
+    __nv_bfloat16* rope = reinterpret_cast<__nv_bfloat16*>(rowp + rope_off);
+    for (int j = threadIdx.x; j < a.c; j += blockDim.x) {
+      const float v = fin[j];
+      if (j >= r0) {
+        rope[j - r0] = __float2bfloat16_rn(v);
+        continue;
+      }
+      const int E = state::kv_mx_exponent(warp_max(fabsf(v)));
+      const uint32_t code = state::e2m1_code(v / state::pow2f(E));
+      const uint32_t hi = __shfl_xor_sync(0xffffffffu, code, 1);
+      if ((j & 1) == 0) rowp[j >> 1] = (uint8_t)(code | (hi << 4));
+      if ((j & 31) == 0) exps[j >> 5] = (uint8_t)(E + 127);
+    }
+    const int pad = (int)(rope_off - state::fp4_exps_offset(a.c, a.rope_dims)) - r0 / 32;
+    if (threadIdx.x < pad) exps[r0 / 32 + threadIdx.x] = 0;
+    return;
+  }
   if (a.out == state::kOutFp8) {
     const float scale = state::fp8_row_scale(block_max_nonneg(amax, red));
     uint8_t* codes = static_cast<uint8_t*>(a.pages) + off;

@@ -23,6 +23,11 @@
 // and the KV entries in the mixed precision of 一(三)4 item 1:
 //   mixed: c + r bytes per row, the e4m3 codes of the first c-r values (one fp32 row scale,
 //     amax of those values / 448) then the last r (RoPE) values as bf16.
+// or in about four bits a value:
+//   mixed MXFP4: the e2m1 pairs of the first c-r values, one e8m0 exponent per 32 of them
+//     (padded with zero bytes to 16), then the last r (RoPE) values as bf16. The exponent is
+//     held to [-14, 13], so that every value is an f16 number (the operands of the attention
+//     that reads it); magnitudes above 6 * 2^13 saturate.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -47,7 +52,8 @@ enum {
   kErrPageId = -3    // page table entry outside [0, n_pages)
 };
 
-enum { kOutIo = 0, kOutFp8 = 1, kOutMxfp4 = 2, kOutMixed = 3 };  // storage of finished rows
+enum { kOutIo = 0, kOutFp8 = 1, kOutMxfp4 = 2, kOutMixed = 3,
+       kOutMixedFp4 = 4 };  // storage of finished rows
 
 struct Args {
   int B, m, c, overlap, rope_dims, finalize, n_win, n_pages, page_rows, max_pages, out;
@@ -230,6 +236,20 @@ CSA_HD int mx_exponent(float amax) {
   const int E = e - 1 - 2;
   return E < -127 ? -127 : (E > 127 ? 127 : E);
 }
+
+// The same exponent for a block of a 4-bit KV row, held to the range whose products are f16.
+CSA_HD int kv_mx_exponent(float amax) {
+  if (amax >= 65536.f) return 13;
+  const int E = mx_exponent(amax);
+  return E < -14 ? -14 : (E > 13 ? 13 : E);
+}
+
+// Bytes of a 4-bit KV row and the offsets of its exponents and RoPE values.
+CSA_HD size_t fp4_exps_offset(int c, int r) { return (size_t)(c - r) / 2; }
+CSA_HD size_t fp4_rope_offset(int c, int r) {
+  return fp4_exps_offset(c, r) + (size_t)(((c - r) / 32 + 15) / 16 * 16);
+}
+CSA_HD size_t fp4_row_bytes(int c, int r) { return fp4_rope_offset(c, r) + 2 * (size_t)r; }
 
 // 2^E as a float (E = -127 is a subnormal).
 CSA_HD float pow2f(int E) {
