@@ -364,6 +364,55 @@ csa_status csa_index_topk_paged(const csa_params* p, int32_t B, int32_t T,
                                 void* stream);
 
 /*
+ * Accumulated attention weight per cache entry, over the queries of a call:
+ *   acc[b, e] = decay * acc[b, e] + sum over t < T and heads h of p(b, t, h, e),
+ *   p = e^z / (sum of e^z over the query's rows + e^{sink[h]}),
+ * z and the rows as in csa_sparse_mqa_paged (idx given: the listed entries, k = p->topk) or
+ * hca_dense_mqa_paged (idx NULL: every visible entry), window and sink in the denominator. It is
+ * what csa_evict_pages chooses by: call it beside the attention, on every decode step or every
+ * few, or on the last queries of a prefill. acc: fp32 [B, N_cap], N_cap = page_rows * max_pages,
+ * updated in place (every entry decays; an entry listed twice gets both weights). kv->fmt is
+ * CSA_BF16 or CSA_MIXED_MXFP4_BF16, else CSA_ERR_UNSUPPORTED. Logits, sums and weights are fp32
+ * (q_hat enters the products as two 16-bit parts); the same inputs give the same bits. decay in
+ * [0, 1]. c = 512, rope_dims = 64, n_heads a multiple of 64, B * T <= 65535 and T * n_heads <=
+ * 2^22. With B * T = 0 acc is left as it is. Pages and evicted pages as in the attention (device
+ * error code 226). Workspace: csa_attn_mass_workspace_size (sparse = 1 with an index list):
+ * 4 bytes per (query, head, row).
+ */
+csa_status csa_attn_mass_paged(const csa_params* p, int32_t B, int32_t T, const void* q,
+                               const int64_t* q_pos, const csa_paged_kv* kv, const int32_t* idx,
+                               const void* win_kv, int64_t L_raw, const int64_t* win_pos0,
+                               const float* sink, const void* q_rms_w, float decay, float* acc,
+                               void* ws, size_t ws_bytes, void* stream);
+size_t csa_attn_mass_workspace_size(const csa_params* p, int32_t B, int32_t T, int64_t N_cap,
+                                    int32_t sparse);
+
+/*
+ * Which pages of each request stay when it may keep `budget` of them. pos[b] is the position of
+ * request b's newest token (csa_state_append's), so that it has min(floor((pos + 1) / m), N_cap)
+ * entries, in its first `used` pages; a page whose table entry is negative holds none. A page's
+ * score is the largest acc of its entries (a NaN counts as the lowest). The first keep_first and
+ * the last keep_last of the `used` pages stay (keep_last >= 1 keeps the page being filled), and
+ * the best scored others fill the budget; among equal scores the lower page stays. Written whole:
+ *   new_table int32 [B, max_pages]: page_table with -2 at the evicted pages (it may be
+ *     page_table itself);
+ *   kept int32 [B, budget]: the kept logical pages, ascending, then -1;
+ *   entries int32 [B, budget * page_rows] or NULL: their entries, ascending, then -1: the index
+ *     list with which csa_sparse_mqa_paged attends to what is left (p->topk = budget *
+ *     page_rows, at most 2048);
+ *   evicted int32 [B, max_pages]: the evicted logical pages, ascending, then -1;
+ *   counts int32 [B, 3]: kept pages, their entries, evicted pages.
+ * Entries keep their numbers, and nothing is moved. On the host, csa_page_alloc_evict gives the
+ * evicted pages back to their pool. Workspace: csa_evict_pages_workspace_size.
+ */
+csa_status csa_evict_pages(const csa_params* p, int32_t B, int32_t page_rows, int32_t max_pages,
+                           const int64_t* pos, const float* acc, const int32_t* page_table,
+                           int32_t budget, int32_t keep_first, int32_t keep_last,
+                           int32_t* new_table, int32_t* kept, int32_t* entries, int32_t* evicted,
+                           int32_t* counts, void* ws, size_t ws_bytes, void* stream);
+size_t csa_evict_pages_workspace_size(int32_t B, int32_t max_pages);
+
+/*
  * The CSA layer over the state cache's paged caches: csa_index_topk_paged on `keys`
  * (optionally with BF16 index scores), then the sparse MQA over `kv` (bf16 or mixed rows,
  * as csa_sparse_mqa_paged), in one call with the decode chain of csa_forward. io = bf16 for
@@ -421,6 +470,8 @@ csa_status csa_state_resume(const csa_params* p, csa_dtype io, int32_t B, int64_
  *     pages for those not yet mapped (mapped ones stay). CSA_ERR_NO_PAGES, with nothing
  *     taken, when too few are free.
  *   csa_page_alloc_release: gives all of request b's pages back; its row becomes -1.
+ *   csa_page_alloc_evict: gives the n logical pages (ascending, mapped; host array) of request b
+ *     back and marks them -2 (evicted); reserve does not map them again. All or nothing.
  *   csa_page_alloc_table: the host table [B, max_pages] (valid until destroy).
  *   csa_page_alloc_free_pages / csa_page_alloc_mapped: free pages in the pool / logical pages
  *     mapped for request b (-1 for an invalid handle or b).
@@ -434,6 +485,7 @@ csa_status csa_page_alloc_create(int32_t n_pages, int32_t B, int32_t max_pages,
 void csa_page_alloc_destroy(csa_page_alloc* a);
 csa_status csa_page_alloc_reserve(csa_page_alloc* a, int32_t b, int32_t n_logical);
 csa_status csa_page_alloc_release(csa_page_alloc* a, int32_t b);
+csa_status csa_page_alloc_evict(csa_page_alloc* a, int32_t b, const int32_t* pages, int32_t n);
 const int32_t* csa_page_alloc_table(const csa_page_alloc* a);
 int32_t csa_page_alloc_free_pages(const csa_page_alloc* a);
 int32_t csa_page_alloc_mapped(const csa_page_alloc* a, int32_t b);
@@ -542,7 +594,7 @@ void csa_set_index_timing_events(void* const* before, void* const* after, int32_
  * early instead of hanging. csa_state_append also leaves a code for a request it skipped.
  * Codes by kernel family: 101-107 MXFP4 indexer (107: a page id outside the pool), 201-205
  * attention (205: a page id outside the pool), 211-216 attention over 4-bit rows (216: a page id
- * outside the pool), 301-309 FP8 / bf16 indexer (309: a page id
+ * outside the pool), 221-226 attention weight (226: likewise), 301-309 FP8 / bf16 indexer (309: a page id
  * outside the pool), 321-323 state append, 324-325 encoding into pages, 331 paged
  * compression, 401-405 prefill output projection. Writes the code to *code (0 = none) and clears it. Synchronises the device.
  * Returns CSA_ERR_CUDA if the copy fails.

@@ -33,6 +33,8 @@ EXPORTS = (
     "csa_page_alloc_create", "csa_page_alloc_destroy", "csa_page_alloc_reserve",
     "csa_page_alloc_release", "csa_page_alloc_table", "csa_page_alloc_free_pages",
     "csa_page_alloc_mapped", "csa_state_pages_needed", "csa_encode_paged",
+    "csa_attn_mass_paged", "csa_attn_mass_workspace_size", "csa_evict_pages",
+    "csa_evict_pages_workspace_size", "csa_page_alloc_evict",
 )
 # size of the library-owned scratch array behind csa_topk_noalloc (bytes, per device)
 TOPK_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -128,10 +130,19 @@ _SIGS = {
     "csa_page_alloc_free_pages": [_VP],
     "csa_page_alloc_mapped": [_VP, _I32],
     "csa_state_pages_needed": [_I32, _I32, _I64],
+    "csa_attn_mass_paged": [_PP, _I32, _I32, _VP, _VP, ctypes.POINTER(CsaPagedKv), _VP, _VP, _I64,
+                            _VP, _VP, _VP, ctypes.c_float, _VP, _VP, _SZ, _VP],
+    "csa_attn_mass_workspace_size": [_PP, _I32, _I32, _I64, _I32],
+    "csa_evict_pages": [_PP, _I32, _I32, _I32, _VP, _VP, _VP, _I32, _I32, _I32] + [_VP] * 6 +
+                       [_SZ, _VP],
+    "csa_evict_pages_workspace_size": [_I32, _I32],
+    "csa_page_alloc_evict": [_VP, _I32, _VP, _I32],
     "csa_encode_paged": [_PP, ctypes.c_int, _I32, _I64, _I64, _VP, ctypes.POINTER(CsaPagedKv),
                          _VP],
 }
-_RES = {"csa_workspace_size": _SZ, "csa_grouped_out_proj_workspace_size": _SZ, "csa_kernel_launches": ctypes.c_uint64, "csa_status_string": ctypes.c_char_p,
+_RES = {"csa_workspace_size": _SZ, "csa_grouped_out_proj_workspace_size": _SZ,
+        "csa_attn_mass_workspace_size": _SZ, "csa_evict_pages_workspace_size": _SZ,
+        "csa_kernel_launches": ctypes.c_uint64, "csa_status_string": ctypes.c_char_p,
         "csa_last_error": ctypes.c_char_p, "csa_version": ctypes.c_char_p,
         "csa_set_index_timing_events": None, "csa_page_alloc_destroy": None,
         "csa_page_alloc_table": ctypes.POINTER(ctypes.c_int32),
@@ -222,6 +233,12 @@ class PageAlloc:
 
     def release(self, b: int) -> None:
         _check("csa_page_alloc_release", lib().csa_page_alloc_release(self._h, b))
+
+    def evict(self, b: int, pages) -> None:
+        """Give the ascending logical pages (e.g. csa_evict_pages' list) of request b back."""
+        pages = [int(x) for x in pages]
+        arr = (_I32 * max(len(pages), 1))(*pages)
+        _check("csa_page_alloc_evict", lib().csa_page_alloc_evict(self._h, b, arr, len(pages)))
 
     @property
     def table(self):
@@ -388,6 +405,33 @@ def hca_dense_mqa_paged(p, B, T, q, q_pos, kv: CsaPagedKv, win_kv, L_raw, win_po
                                   _ptr(win_kv), L_raw, _ptr(win_pos0), _ptr(sink),
                                   _ptr(q_rms_w), _ptr(out), _ptr(ws), ws_bytes, _stream(stream))
     _check("hca_dense_mqa_paged", s)
+
+
+def attn_mass_workspace_size(p, B, T, N_cap, sparse) -> int:
+    return int(lib().csa_attn_mass_workspace_size(ctypes.byref(p), B, T, N_cap, int(sparse)))
+
+
+def csa_attn_mass_paged(p, B, T, q, q_pos, kv: CsaPagedKv, idx, win_kv, L_raw, win_pos0, sink,
+                        q_rms_w, decay, acc, ws, ws_bytes, stream=None):
+    s = lib().csa_attn_mass_paged(ctypes.byref(p), B, T, _ptr(q), _ptr(q_pos), ctypes.byref(kv),
+                                  _ptr(idx), _ptr(win_kv), L_raw, _ptr(win_pos0), _ptr(sink),
+                                  _ptr(q_rms_w), decay, _ptr(acc), _ptr(ws), ws_bytes,
+                                  _stream(stream))
+    _check("csa_attn_mass_paged", s)
+
+
+def evict_pages_workspace_size(B, max_pages) -> int:
+    return int(lib().csa_evict_pages_workspace_size(B, max_pages))
+
+
+def csa_evict_pages(p, B, page_rows, max_pages, pos, acc, page_table, budget, keep_first,
+                    keep_last, new_table, kept, entries, evicted, counts, ws, ws_bytes,
+                    stream=None):
+    s = lib().csa_evict_pages(ctypes.byref(p), B, page_rows, max_pages, _ptr(pos), _ptr(acc),
+                              _ptr(page_table), budget, keep_first, keep_last, _ptr(new_table),
+                              _ptr(kept), _ptr(entries), _ptr(evicted), _ptr(counts), _ptr(ws),
+                              ws_bytes, _stream(stream))
+    _check("csa_evict_pages", s)
 
 
 def csa_index_topk_paged(p, B, T, keys: CsaPagedKv, qI, qI_scale, w, q_pos, bf16_scores, out_idx,

@@ -273,7 +273,7 @@ const char* csa_last_error(void) { return g_err; }
 
 csa_status csa_device_error(int32_t* code) {
   REQUIRE(code != nullptr, "code is NULL");
-  int words[7] = {0, 0, 0, 0, 0, 0, 0};
+  int words[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   TRY(cuda_status(csa::index_mxf4_device_error(&words[0]), "device error word"));
   TRY(cuda_status(csa::mqa_tc_device_error(&words[1]), "device error word"));
   TRY(cuda_status(csa::index_bf16_device_error(&words[2]), "device error word"));
@@ -281,6 +281,7 @@ csa_status csa_device_error(int32_t* code) {
   TRY(cuda_status(csa::out_proj_tc_device_error(&words[4]), "device error word"));
   TRY(cuda_status(csa::compress_device_error(&words[5]), "device error word"));
   TRY(cuda_status(csa::attn_fp4_device_error(&words[6]), "device error word"));
+  TRY(cuda_status(csa::attn_mass_device_error(&words[7]), "device error word"));
   *code = 0;
   for (int w : words)
     if (*code == 0) *code = w;
@@ -963,6 +964,111 @@ csa_status hca_dense_mqa_paged(const csa_params* p, int32_t B, int32_t T, const 
   TRY(paged_layout(kv, &lay, &N_cap));
   return tc_mqa_ext("dense MQA (paged KV)", p, B, T, q, q_pos, lay, N_cap, nullptr, 0, win_kv,
                     L_raw, win_pos0, sink, q_rms_w, out, ws, ws_bytes, stream);
+}
+
+namespace {
+// sizes, shape and method constants of the attention weight, the same for its workspace query
+csa_status check_mass(const csa_params* p, int32_t B, int32_t T, int64_t N_cap, bool sparse) {
+  TRY(check_params(p));
+  TRY(check_attn(p));
+  TRY(check_sizes(B, T, N_cap));
+  if (sparse) TRY(check_topk(p));
+  REQUIRE((int64_t)B * T <= 65535, "the attention weight takes at most 65535 queries per call");
+  REQUIRE((int64_t)T * p->n_heads <= (1 << 22), "T * n_heads too large");
+  auto a = make_mqa(p, B, T, nullptr, nullptr, nullptr, N_cap, nullptr, sparse ? p->topk : 0,
+                    nullptr, 0, nullptr, nullptr, nullptr, nullptr);
+  if (!csa::attn_fp4_supported(a))
+    return fail(CSA_ERR_UNSUPPORTED,
+                "the attention weight needs c = 512, rope_dims = 64 and n_heads a multiple of 64");
+  return CSA_OK;
+}
+}  // namespace
+
+size_t csa_attn_mass_workspace_size(const csa_params* p, int32_t B, int32_t T, int64_t N_cap,
+                                    int32_t sparse) {
+  if (check_mass(p, B, T, N_cap, sparse != 0) != CSA_OK || (int64_t)B * T == 0) return 0;
+  return csa::attn_mass_workspace_bytes(make_mqa(p, B, T, nullptr, nullptr, nullptr, N_cap, nullptr,
+                                                 sparse != 0 ? p->topk : 0, nullptr, 0, nullptr,
+                                                 nullptr, nullptr, nullptr));
+}
+
+csa_status csa_attn_mass_paged(const csa_params* p, int32_t B, int32_t T, const void* q,
+                               const int64_t* q_pos, const csa_paged_kv* kv, const int32_t* idx,
+                               const void* win_kv, int64_t L_raw, const int64_t* win_pos0,
+                               const float* sink, const void* q_rms_w, float decay, float* acc,
+                               void* ws, size_t ws_bytes, void* stream) {
+  TRY(check_params(p));
+  KvLayout lay;
+  int64_t N_cap = 0;
+  TRY(paged_layout(kv, &lay, &N_cap));
+  REQUIRE(std::isfinite(decay) && decay >= 0.f && decay <= 1.f, "decay must be in [0, 1]");
+  TRY(check_mqa_args(p, CSA_BF16, B, T, q, q_pos, kv->pages, N_cap, win_kv, L_raw, win_pos0, sink,
+                     q_rms_w, acc, true));
+  TRY(check_mass(p, B, T, N_cap, idx != nullptr));
+  if (lay.mixed)
+    return fail(CSA_ERR_UNSUPPORTED, "the attention weight reads bf16 or 4-bit rows");
+  if ((int64_t)B * T == 0) return ok();
+  OPTIONAL_PTR(idx);
+  const size_t need = csa_attn_mass_workspace_size(p, B, T, N_cap, idx != nullptr);
+  if (ws == nullptr || ws_bytes < need || !aligned16(ws))
+    return fail(CSA_ERR_WORKSPACE, "the attention weight needs %zu workspace bytes (got %zu)", need,
+                ws_bytes);
+  auto a = make_mqa(p, B, T, q, q_pos, lay.rows, N_cap, idx, idx != nullptr ? p->topk : 0, win_kv,
+                    L_raw, win_pos0, sink, q_rms_w, nullptr);
+  set_pages(&a, lay);
+  a.fp4 = lay.fp4;
+  TRY(cuda_status(csa::launch_attn_mass(a, decay, acc, ws, (cudaStream_t)stream),
+                  "attention weight"));
+  return ok();
+}
+
+namespace {
+csa_status check_evict_sizes(int32_t B, int32_t max_pages) {
+  REQUIRE(B >= 0 && B <= 65535, "B must be in [0, 65535]");
+  REQUIRE(max_pages >= 1 && max_pages <= (1 << 30), "max_pages must be in [1, 2^30]");
+  return CSA_OK;
+}
+}  // namespace
+
+size_t csa_evict_pages_workspace_size(int32_t B, int32_t max_pages) {
+  if (check_evict_sizes(B, max_pages) != CSA_OK || B == 0) return 0;
+  return csa::evict_workspace_bytes(B, max_pages);
+}
+
+csa_status csa_evict_pages(const csa_params* p, int32_t B, int32_t page_rows, int32_t max_pages,
+                           const int64_t* pos, const float* acc, const int32_t* page_table,
+                           int32_t budget, int32_t keep_first, int32_t keep_last,
+                           int32_t* new_table, int32_t* kept, int32_t* entries, int32_t* evicted,
+                           int32_t* counts, void* ws, size_t ws_bytes, void* stream) {
+  TRY(check_params(p));
+  TRY(check_evict_sizes(B, max_pages));
+  REQUIRE(page_rows >= 1, "page_rows must be >= 1");
+  REQUIRE((int64_t)page_rows * max_pages <= INT32_MAX, "page_rows * max_pages too large");
+  REQUIRE(keep_first >= 0 && keep_last >= 0 && budget >= 1, "budget must be >= 1, keep_first and "
+          "keep_last >= 0");
+  REQUIRE((int64_t)keep_first + keep_last <= budget, "the budget (%d pages) must hold the first %d "
+          "and the last %d pages", budget, keep_first, keep_last);
+  REQUIRE((int64_t)budget * page_rows <= INT32_MAX, "budget * page_rows too large");
+  if (B == 0) return ok();
+  REQUIRE_PTR(pos);
+  REQUIRE_PTR(acc);
+  REQUIRE_PTR(page_table);
+  REQUIRE_PTR(new_table);
+  REQUIRE_PTR(kept);
+  OPTIONAL_PTR(entries);
+  REQUIRE_PTR(evicted);
+  REQUIRE_PTR(counts);
+  const size_t need = csa_evict_pages_workspace_size(B, max_pages);
+  if (ws == nullptr || ws_bytes < need || !aligned16(ws))
+    return fail(CSA_ERR_WORKSPACE, "page eviction needs %zu workspace bytes (got %zu)", need,
+                ws_bytes);
+  csa::EvictArgs a{};
+  a.B = B; a.m = p->m; a.page_rows = page_rows; a.max_pages = max_pages; a.budget = budget;
+  a.keep_first = keep_first; a.keep_last = keep_last; a.pos = pos; a.acc = acc;
+  a.page_table = page_table; a.new_table = new_table; a.kept = kept; a.entries = entries;
+  a.evicted = evicted; a.counts = counts;
+  TRY(cuda_status(csa::launch_evict(a, ws, (cudaStream_t)stream), "page eviction"));
+  return ok();
 }
 
 csa_status csa_forward(const csa_params* p, csa_dtype io, int32_t B, int32_t T,

@@ -169,8 +169,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
   const uint32_t tmem = S.tmem_slot;
 
   if (warp >= 6) {
-    gather_loop<kFp4>(base + kOffKV, kBuf, c0, c1, l.nc, warp - 6, S.ring, S.kv_full, S.kv_free,
-                      kErrGather);
+    gather_loop<kFp4, kBuf, false>(base + kOffKV, c0, c1, l.nc, warp - 6, S.ring, S.kv_full,
+                                   S.kv_free, kErrGather);
   } else if (warp == 5) {
     resolve_rows<kFp4>(a, l, bt, b, c0, c1, S.ring, kErrRing);
   } else if (warp == 4) {

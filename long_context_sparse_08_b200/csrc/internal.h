@@ -176,6 +176,23 @@ bool attn_fp4_supported(const MqaArgs& a);
 size_t attn_fp4_workspace_bytes(const MqaArgs& a);
 cudaError_t launch_attn_fp4(const MqaArgs& a, void* ws, size_t ws_bytes, cudaStream_t st);
 cudaError_t attn_fp4_device_error(int* code);
+
+// accumulated attention weight per entry (4-bit or bf16 pages; the same shapes)
+size_t attn_mass_workspace_bytes(const MqaArgs& a);
+cudaError_t launch_attn_mass(const MqaArgs& a, float decay, float* acc, void* ws, cudaStream_t st);
+cudaError_t attn_mass_device_error(int* code);
+
+// page eviction by that weight
+constexpr int32_t kEvicted = -2;  // page table entry of a page given back
+struct EvictArgs {
+  int B, m, page_rows, max_pages, budget, keep_first, keep_last;
+  const int64_t* pos;         // [B] position of each request's newest token
+  const float* acc;           // [B, page_rows * max_pages]
+  const int32_t* page_table;  // [B, max_pages]
+  int32_t *new_table, *kept, *entries, *evicted, *counts;  // entries may be nullptr
+};
+size_t evict_workspace_bytes(int B, int max_pages);
+cudaError_t launch_evict(const EvictArgs& a, void* ws, cudaStream_t st);
 cudaError_t launch_mqa(const MqaArgs& a, bool bf16, void* ws, size_t ws_bytes, cudaStream_t st);
 
 // Records a formatted message as the calling thread's csa_last_error() and returns `s`.

@@ -32,7 +32,6 @@ constexpr int kAtoms = kC / 64;    // 64-value (128 B) atoms of a row
 constexpr int kAtomBytes = kRows * 128;
 constexpr int kFp4RowBytes = 368, kFp4Exps = 224, kFp4Rope = 240;
 constexpr int kRing = 4;           // chunks of resolved addresses
-constexpr int32_t kEvictedPage = -2;
 
 enum Fmt { kFp4 = 0, kBf16 = 1 };
 
@@ -90,7 +89,7 @@ __device__ __forceinline__ void resolve_rows(const MqaArgs& a, const List& l, in
     for (int i = 0; i < kRing; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        pg[i][h] = kEvictedPage;
+        pg[i][h] = kEvicted;
         if (e[i][h] >= 0 && e[i][h] < a.n_cap)
           pg[i][h] = a.page_table[(size_t)b * a.max_pages + (uint32_t)e[i][h] / (uint32_t)a.page_rows];
       }
@@ -106,7 +105,7 @@ __device__ __forceinline__ void resolve_rows(const MqaArgs& a, const List& l, in
           if (p >= 0 && p < a.n_pages) {
             const size_t row = (size_t)p * a.page_rows + (uint32_t)e[i][h] % (uint32_t)a.page_rows;
             src[h] = reinterpret_cast<uint64_t>(a.kv) + row * row_bytes;
-          } else if (p != kEvictedPage) {
+          } else if (p != kEvicted) {
             set_error(code + 5);
           }
         } else {
@@ -305,26 +304,27 @@ __device__ __forceinline__ float unpack_hi(uint32_t w) {
   else return __uint_as_float(w & 0xffff0000u);
 }
 
-// The gather warps' loop over chunks [c0, c1): `bufs` KV buffers of kAtoms atoms at `kv`, a
-// full barrier per (buffer, atom) and a free barrier per buffer. Loads of a chunk are issued
-// before the wait for its buffer.
-template <int kFmt>
-__device__ __forceinline__ void gather_loop(uint8_t* kv, int bufs, int c0, int c1, int nc,
-                                            int atom, AddrRing& ring, uint64_t* full,
-                                            uint64_t* free, int code) {
+// The gather warps' loop over chunks [c0, c1): kBufs KV buffers of kAtoms atoms at `kv`, a full
+// barrier per (buffer, atom) and a free barrier per buffer, or per (buffer, atom) with
+// kAtomFree (a kernel that reads each atom once may give it back alone). Loads of a chunk are
+// issued before the wait for its buffer.
+template <int kFmt, int kBufs, bool kAtomFree>
+__device__ __forceinline__ void gather_loop(uint8_t* kv, int c0, int c1, int nc, int atom,
+                                            AddrRing& ring, uint64_t* full, uint64_t* free,
+                                            int code) {
   const int lane = threadIdx.x & 31;
   Held v;
   bool ok = true;
   for (int j = c0; j < c1 && ok; ++j) {
-    const int it = j - c0, rs = it % kRing, slot = it % bufs;
+    const int it = j - c0, rs = it % kRing, slot = it % kBufs;
     ok = __all_sync(0xffffffffu, mbar_wait(&ring.full[rs], (uint32_t)(it / kRing) & 1, code));
     if (!ok) break;
     const bool cache = j < nc;
     load_atom<kFmt>(v, ring.src[rs], cache, atom);
     __syncwarp();
     if (lane == 0) mbar_arrive(&ring.free[rs]);
-    ok = __all_sync(0xffffffffu,
-                    mbar_wait(&free[slot], ((uint32_t)(it / bufs) & 1) ^ 1, code + 1));
+    ok = __all_sync(0xffffffffu, mbar_wait(&free[kAtomFree ? slot * kAtoms + atom : slot],
+                                           ((uint32_t)(it / kBufs) & 1) ^ 1, code + 1));
     if (!ok) break;
     store_atom<kFmt>(v, kv + (size_t)(slot * kAtoms + atom) * kAtomBytes, cache, atom);
     fence_proxy_async_smem();

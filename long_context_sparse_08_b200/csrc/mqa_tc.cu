@@ -54,7 +54,6 @@ constexpr int kThreads = 160;    // warps 0-3: loads + softmax + epilogue; warp 
 constexpr int kAtoms = kC / 64;  // 64-element (128 B) swizzle atoms along a row
 constexpr float kLazy = 8.f;     // rescale threshold (natural-log units)
 constexpr int kMaxPairs = 256;   // RoPE pairs (r / 2)
-constexpr int32_t kEvictedPage = -2;  // page table entry of a page given back: masked quietly
 
 // Shared memory (offsets from a 1024-aligned base) for chunks of kR KV rows: kR = 128 with
 // one KV buffer, or kR = 64 with two (the next chunk's rows arrive while this one's products
@@ -199,7 +198,7 @@ __device__ __forceinline__ const void* row_src_ext(const MqaArgs& a, int bt, int
       const int32_t pg =
           pg_hint >= -1 ? pg_hint : a.page_table[(size_t)b * a.max_pages + e / a.page_rows];
       if (pg < 0 || pg >= a.n_pages) {
-        if (pg != kEvictedPage) set_error(kErrPageId);
+        if (pg != kEvicted) set_error(kErrPageId);
         return nullptr;
       }
       row = (size_t)pg * a.page_rows + (size_t)(e % a.page_rows);

@@ -11,6 +11,8 @@
 //
 // Free pages form a FIFO: the pool starts as 0 .. n_pages-1 and a released request's
 // pages join the back in logical order, so a page just given back is the last to be reused.
+// A request may also give single pages back (csa_page_alloc_evict): their logical pages stay
+// marked as evicted, so that a later reservation does not map them again.
 #include <cstdint>
 #include <cstdio>
 #include <deque>
@@ -23,7 +25,7 @@
 struct csa_page_alloc {
   int32_t n_pages, B, max_pages;
   std::deque<int32_t> free_list;
-  std::vector<int32_t> table;   // [B, max_pages], -1 = not mapped
+  std::vector<int32_t> table;   // [B, max_pages], -1 = not mapped, -2 = evicted
   std::vector<int32_t> mapped;  // [B]: logical pages 0 .. mapped[b]-1 are mapped
 };
 
@@ -81,10 +83,30 @@ csa_status csa_page_alloc_release(csa_page_alloc* a, int32_t b) {
     return csa::report_error(CSA_ERR_INVALID_ARG, "request %d outside [0, %d)", b, a->B);
   int32_t* row = a->table.data() + (size_t)b * a->max_pages;
   for (int32_t k = 0; k < a->mapped[b]; ++k) {
-    a->free_list.push_back(row[k]);
+    if (row[k] >= 0) a->free_list.push_back(row[k]);
     row[k] = -1;
   }
   a->mapped[b] = 0;
+  return csa::report_error(CSA_OK, "");
+}
+
+csa_status csa_page_alloc_evict(csa_page_alloc* a, int32_t b, const int32_t* pages, int32_t n) {
+  if (a == nullptr) return csa::report_error(CSA_ERR_INVALID_ARG, "allocator is NULL");
+  if (b < 0 || b >= a->B)
+    return csa::report_error(CSA_ERR_INVALID_ARG, "request %d outside [0, %d)", b, a->B);
+  if (n < 0 || (n > 0 && pages == nullptr))
+    return csa::report_error(CSA_ERR_INVALID_ARG, "a list of n >= 0 pages is needed");
+  int32_t* row = a->table.data() + (size_t)b * a->max_pages;
+  for (int32_t i = 0; i < n; ++i)
+    if (pages[i] < 0 || pages[i] >= a->mapped[b] || row[pages[i]] < 0 ||
+        (i > 0 && pages[i] <= pages[i - 1]))
+      return csa::report_error(CSA_ERR_INVALID_ARG,
+                               "logical page %d of request %d is not mapped, or the list is not "
+                               "ascending", pages[i], b);
+  for (int32_t i = 0; i < n; ++i) {
+    a->free_list.push_back(row[pages[i]]);
+    row[pages[i]] = csa::kEvicted;
+  }
   return csa::report_error(CSA_OK, "");
 }
 
