@@ -189,14 +189,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
                               mbar_wait(&S.kv_full[slot * kAtoms + atom], ph, kErrMma));
         if (!ok) return;
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
 #pragma unroll
           for (int kq = 0; kq < 4; ++kq)
             mma_f16(tmem + kColS + 64 * slot, dq + ((atom * (kHg * 128) + kq * 32) >> 4),
                     dk + ((atom * kAtomBytes + kq * 32) >> 4), idS, (atom | kq) != 0 ? 1u : 0u);
         }
       }
-      if (lane == 0) mma_commit(&S.s_full[slot]);
+      if (elect_one()) mma_commit(&S.s_full[slot]);
       __syncwarp();
     };
     if (ok) issue_s(c0);
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
       ok = __all_sync(0xffffffffu, mbar_wait(&S.p_full[slot], (uint32_t)(it / kBuf) & 1, kErrMma));
       if (!ok) break;
       tc_fence_after();
-      if (lane == 0) {
+      if (elect_one()) {
         const uint64_t dv = smem_desc(smem_u32(base + kOffKV + slot * kSlotKV), kAtomBytes, 1024,
                                       kLayoutSw128);
         const uint64_t dp = smem_desc(smem_u32(base + kOffP + slot * kSlotP), 16, 1024, kLayoutSw128);
@@ -225,11 +225,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
       }
       __syncwarp();
     }
-    if (lane == 0) {  // nothing this thread issued is in flight once `done` fires
-      mma_commit(&S.done);
-      mbar_wait(&S.done, 0, kErrMma);
-    }
     __syncwarp();
+    if (elect_one()) mma_commit(&S.done);  // fires when nothing issued here is in flight
+    __syncwarp();
+    mbar_wait(&S.done, 0, kErrMma);
   } else {
     // ---- q_hat: a warp per head, eight heads in flight ----
     {

@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mass_logits(const __grid_consta
         ok = ok && __all_sync(0xffffffffu, mbar_wait(&S.kv_full[atom], (uint32_t)it & 1, kErrMma));
         if (!ok) break;
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
 #pragma unroll
           for (int kq = 0; kq < 4; ++kq)
             mma_f16(tmem + 64 * slot, dq + ((atom * kQAtom + kq * 32) >> 4),
@@ -143,14 +143,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_mass_logits(const __grid_consta
         }
       }
       if (!ok) break;
-      if (lane == 0) mma_commit(&S.s_full[slot]);
+      if (elect_one()) mma_commit(&S.s_full[slot]);
       __syncwarp();
     }
-    if (lane == 0) {  // nothing this thread issued is in flight once `done` fires
-      mma_commit(&S.done);
-      mbar_wait(&S.done, 0, kErrMma);
-    }
     __syncwarp();
+    if (elect_one()) mma_commit(&S.done);  // fires when nothing issued here is in flight
+    __syncwarp();
+    mbar_wait(&S.done, 0, kErrMma);
   } else {
     // ---- q_hat = hi + lo, a warp per head, eight heads in flight ----
     {
