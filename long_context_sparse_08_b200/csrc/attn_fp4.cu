@@ -12,12 +12,12 @@
 // and split over `nsplit` CTAs. Per chunk, with f16 operands in 128B-swizzled shared memory
 // and fp32 accumulators in TMEM:
 //   S[64 heads x 64 rows] = q_hat . K^T          (M = 64; A = q_hat, B = the KV tile)
-//   P = 2^(S * scale * log2(e) - m_h) in f16     (two threads a head)
+//   P = 2^(S * scale * log2(e) - m_h) in f16     (four threads a head)
 //   O^T[4 x 128 dims x 64 heads] += V^T . P^T    (A = the same KV tile read MN-major)
-// Warps: 0-3 prepare q_hat, then softmax and epilogue; 4 issues the MMAs; 5 resolves
-// addresses; 6-13 each widen one 64-value atom of every row (kv_rows.cuh). Two KV buffers:
-// S of chunk j + 1 is issued before O^T of chunk j, so the tensor cores work during the
-// softmax, and the gather warps fill the buffer that O^T released.
+// Warps: 0-3 softmax and epilogue; 4 issues the MMAs; 5 resolves addresses; 6-13 each widen
+// one 64-value atom of every row (kv_rows.cuh); 0-3 and 6-13 prepare q_hat first. Two KV
+// buffers: S of chunk j + 1 may be issued before O^T of chunk j, so the tensor cores work
+// during the softmax, and the gather warps fill the buffer that O^T released.
 // The running max m_h is raised only when a chunk's max exceeds it by more than 2^11.5 (then
 // O^T and l are rescaled); P stays below 2^11.5, inside f16, and sums are fp32.
 // One split: the CTA finalises. Several: it writes (m, l, O) partials and k_attn_fp4_combine
@@ -59,7 +59,7 @@ enum { kErrRing = 211, kErrGather = 212, kErrMma = 214, kErrSoftmax = 215 };
 
 struct Smem {
   AddrRing ring;
-  uint64_t kv_full[kBuf * kAtoms], kv_free[kBuf], s_full[kBuf], p_full[kBuf], q_full, done;
+  uint64_t kv_full[kBuf], kv_free[kBuf], s_full[kBuf], p_full[kBuf], q_full, done;
   uint32_t tmem_slot;
   float m_used[kHg], l_sum[kHg], alpha[kHg], fin[kHg];
   RopeTable rope;
@@ -91,11 +91,11 @@ __device__ __forceinline__ bool reduce_softmax(bool p, bool all) {
   return res != 0;
 }
 
-// 16 TMEM lanes x 64 columns, two threads per lane: thread t of the warp gets lane
-// t / 4 + 8 (t % 2) and, in register i, column 2 i + (t / 2) % 2.
-__device__ __forceinline__ void tmem_ld_16x64b_x32(uint32_t taddr, uint32_t* r) {
+// 16 TMEM lanes x 64 columns of 32-bit as eight 16 x 8 pieces: thread t gets, in registers 4 i
+// .. 4 i + 3, columns 8 i + 2 (t % 4), + 1 of lane t / 4 and of lane t / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x64b.x32.b32"
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32"
       " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
       " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31},"
       " [%32];"
@@ -106,6 +106,17 @@ __device__ __forceinline__ void tmem_ld_16x64b_x32(uint32_t taddr, uint32_t* r) 
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
         "=r"(r[31])
       : "r"(taddr));
+}
+__device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                            uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a),
+               "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -129,6 +140,38 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// q_hat of heads first .. first + kN - 1 of the group, by one warp, all of them in flight.
+template <int kN>
+__device__ __forceinline__ void prepare_q(const MqaArgs& a, int bt, int h0, int first, uint8_t* qs,
+                                          const RopeTable& rope) {
+  const int lane = threadIdx.x & 31;
+  const uint4* qg = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                   ((size_t)bt * a.H + h0 + first) * kC);
+  uint4 raw[kN][2];
+#pragma unroll
+  for (int i = 0; i < kN; ++i)
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+      raw[i][half] = __ldg(qg + (size_t)i * (kC / 8) + 32 * half + lane);
+  float w[16];
+  qhat_weights(a.q_rms_w, w);
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    float y[16];
+    qhat_lane(raw[i], w, a.eps, rope, y);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = pack2<kFp4>(y[8 * half + 2 * k], y[8 * half + 2 * k + 1]);
+      const int c = lane + 32 * half;  // 16-byte piece of the row
+      *reinterpret_cast<uint4*>(qs + (c >> 3) * (kHg * 128) + sw128(first + i, c & 7)) =
+          make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+  fence_proxy_async_smem();
+}
+
 __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant__ Params P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_align1024(smem_raw);
@@ -144,13 +187,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
         mbar_init(&S.ring.full[i], 1);
         mbar_init(&S.ring.free[i], 8 + 4);  // gather warps; softmax warps (the mask)
       }
-      for (int i = 0; i < kBuf * kAtoms; ++i) mbar_init(&S.kv_full[i], 1);
       for (int i = 0; i < kBuf; ++i) {
+        mbar_init(&S.kv_full[i], 8);  // the gather warps
         mbar_init(&S.kv_free[i], 1);
         mbar_init(&S.s_full[i], 1);
         mbar_init(&S.p_full[i], 4);
       }
-      mbar_init(&S.q_full, 4);
+      mbar_init(&S.q_full, 12);  // softmax and gather warps
       mbar_init(&S.done, 1);
       fence_barrier_init();
     }
@@ -169,6 +212,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
   const uint32_t tmem = S.tmem_slot;
 
   if (warp >= 6) {
+    prepare_q<4>(a, bt, h0, 32 + 4 * (warp - 6), base + kOffQ, S.rope);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.q_full);
     gather_loop<kFp4, kBuf, false>(base + kOffKV, c0, c1, l.nc, warp - 6, S.ring, S.kv_full,
                                    S.kv_free, kErrGather);
   } else if (warp == 5) {
@@ -179,100 +225,81 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
     const uint32_t idO = idesc_f16(0, 128, kHg) | (1u << 15);  // M = 128 dims; A MN-major
     const uint64_t dq = smem_desc(smem_u32(base + kOffQ), 16, 1024, kLayoutSw128);
     bool ok = c0 < c1 && __all_sync(0xffffffffu, mbar_wait(&S.q_full, 0, kErrMma));
-    auto issue_s = [&](int j) {
-      const int it = j - c0, slot = it % kBuf;
-      const uint32_t ph = (uint32_t)(it / kBuf) & 1;
-      const uint64_t dk = smem_desc(smem_u32(base + kOffKV + slot * kSlotKV), 16, 1024, kLayoutSw128);
-#pragma unroll
-      for (int atom = 0; atom < kAtoms; ++atom) {
-        ok = ok && __all_sync(0xffffffffu,
-                              mbar_wait(&S.kv_full[slot * kAtoms + atom], ph, kErrMma));
-        if (!ok) return;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int kq = 0; kq < 4; ++kq)
-            mma_f16(tmem + kColS + 64 * slot, dq + ((atom * (kHg * 128) + kq * 32) >> 4),
-                    dk + ((atom * kAtomBytes + kq * 32) >> 4), idS, (atom | kq) != 0 ? 1u : 0u);
+    // S runs at most one chunk ahead of O^T. Where both could be issued, whichever has its
+    // operands goes first, O^T before S (it frees a buffer). S tile slot j % 2 was read by the
+    // softmax of chunk j - 2 before it published P(j - 2), which this warp has waited for.
+    int js = c0, jv = c0;
+    long long t0 = clock64();  // of the last step
+    while (ok && jv < c1) {
+      const int iv = jv - c0, is = js - c0;
+      const bool can_v = jv < js, can_s = js < c1 && js - jv < kBuf;
+      uint64_t* const pb = &S.p_full[iv % kBuf];
+      uint64_t* const kb = &S.kv_full[is % kBuf];
+      const uint32_t pp = (uint32_t)(iv / kBuf) & 1, kp = (uint32_t)(is / kBuf) & 1;
+      bool do_v = can_v, do_s = can_s;
+      if (can_v && can_s) {
+        do_v = __any_sync(0xffffffffu, mbar_test(pb, pp));
+        do_s = !do_v && __any_sync(0xffffffffu, mbar_test(kb, kp));
+        if (!do_v && !do_s) {
+          if (clock64() - t0 > kSpinCycles) {
+            set_error(kErrMma);
+            ok = false;
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          continue;
         }
       }
-      if (elect_one()) mma_commit(&S.s_full[slot]);
-      __syncwarp();
-    };
-    if (ok) issue_s(c0);
-    for (int j = c0; j < c1 && ok; ++j) {
-      const int it = j - c0, slot = it % kBuf;
-      if (j + 1 < c1) {
-        // S tile (j + 1) % 2 was read by the softmax of chunk j - 1 before it published P(j - 1),
-        // which this warp has waited for
-        issue_s(j + 1);
-        if (!ok) break;
-      }
-      ok = __all_sync(0xffffffffu, mbar_wait(&S.p_full[slot], (uint32_t)(it / kBuf) & 1, kErrMma));
+      ok = __all_sync(0xffffffffu, mbar_wait(do_v ? pb : kb, do_v ? pp : kp, kErrMma));
       if (!ok) break;
       tc_fence_after();
-      if (elect_one()) {
+      if (do_v) {
+        const int slot = iv % kBuf;
         const uint64_t dv = smem_desc(smem_u32(base + kOffKV + slot * kSlotKV), kAtomBytes, 1024,
                                       kLayoutSw128);
         const uint64_t dp = smem_desc(smem_u32(base + kOffP + slot * kSlotP), 16, 1024, kLayoutSw128);
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < kRows / 16; ++kk)
+          for (int kk = 0; kk < kRows / 16; ++kk)
 #pragma unroll
-          for (int sl = 0; sl < 4; ++sl)
-            mma_f16(tmem + kColO + 64 * sl, dv + ((sl * 2 * kAtomBytes + kk * 2048) >> 4),
-                    dp + ((kk * 32) >> 4), idO, (j > c0 || kk > 0) ? 1u : 0u);
-        mma_commit(&S.kv_free[slot]);
+            for (int sl = 0; sl < 4; ++sl)
+              mma_f16(tmem + kColO + 64 * sl, dv + ((sl * 2 * kAtomBytes + kk * 2048) >> 4),
+                      dp + ((kk * 32) >> 4), idO, (jv > c0 || kk > 0) ? 1u : 0u);
+          mma_commit(&S.kv_free[slot]);
+        }
+        ++jv;
+      } else {
+        const int slot = is % kBuf;
+        const uint64_t dk = smem_desc(smem_u32(base + kOffKV + slot * kSlotKV), 16, 1024, kLayoutSw128);
+        if (elect_one()) {
+#pragma unroll
+          for (int atom = 0; atom < kAtoms; ++atom)
+#pragma unroll
+            for (int kq = 0; kq < 4; ++kq)
+              mma_f16(tmem + kColS + 64 * slot, dq + ((atom * (kHg * 128) + kq * 32) >> 4),
+                      dk + ((atom * kAtomBytes + kq * 32) >> 4), idS, (atom | kq) != 0 ? 1u : 0u);
+          mma_commit(&S.s_full[slot]);
+        }
+        ++js;
       }
       __syncwarp();
+      t0 = clock64();
     }
     __syncwarp();
     if (elect_one()) mma_commit(&S.done);  // fires when nothing issued here is in flight
     __syncwarp();
     mbar_wait(&S.done, 0, kErrMma);
   } else {
-    // ---- q_hat: a warp per head, eight heads in flight ----
-    {
-      float w[16];
-      qhat_weights(a.q_rms_w, w);
-      const uint4* qg = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                       ((size_t)bt * a.H + h0) * kC);
-      uint8_t* qs = base + kOffQ;
-#pragma unroll 1
-      for (int hb = 0; hb < 16; hb += 8) {
-        uint4 raw[8][2];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
-            raw[i][half] = __ldg(qg + (size_t)(16 * warp + hb + i) * (kC / 8) + 32 * half + lane);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int h = 16 * warp + hb + i;
-          float y[16];
-          qhat_lane(raw[i], w, a.eps, S.rope, y);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t o[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              o[k] = pack2<kFp4>(y[8 * half + 2 * k], y[8 * half + 2 * k + 1]);
-            const int c = lane + 32 * half;  // 16-byte piece of the row
-            *reinterpret_cast<uint4*>(qs + (c >> 3) * (kHg * 128) + sw128(h, c & 7)) =
-                make_uint4(o[0], o[1], o[2], o[3]);
-          }
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.q_full);
-    }
+    prepare_q<8>(a, bt, h0, 8 * warp, base + kOffQ, S.rope);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.q_full);
     // ------------------------------ softmax ------------------------------
     const uint32_t lane_base = tmem + ((uint32_t)(32 * warp) << 16);
-    // the M = 64 accumulator puts head 16w + i in TMEM lane 32w + i (i < 16); threads t and
-    // t ^ 2 share head 16w + t / 4 + 8 (t % 2), each with every other row of a chunk
-    const int par = (lane >> 1) & 1;
-    const int hh = 16 * warp + (lane >> 2) + 8 * (lane & 1);
-    float mu = -INFINITY, lsum = 0.f;
+    // The M = 64 accumulator puts head 16w + i in TMEM lane 32w + i (i < 16). Four threads (a
+    // quad) share heads h and h + 8: thread t has columns (rows of the chunk) 8 i + 2 (t % 4),
+    // + 1 of head 16w + t / 4 in s[4i], s[4i + 1] and of that head + 8 in s[4i + 2], s[4i + 3]:
+    // neighbouring rows pair up into one f16x2 of P without an exchange.
+    const int quad = lane & 3, hq = 16 * warp + (lane >> 2);
+    float mu[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
     bool ok = true;
 #pragma unroll 1
     for (int j = c0; j < c1 && ok; ++j) {
@@ -281,31 +308,48 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
       if (!ok) break;
       tc_fence_after();
       uint32_t sv[32];
-      tmem_ld_16x64b_x32(lane_base + kColS + 64 * slot, sv);
-      tmem_ld_wait();
+      tmem_ld_16x256b_x8(lane_base + kColS + 64 * slot, sv);
       const uint32_t vm[2] = {S.ring.mask[rs][0], S.ring.mask[rs][1]};
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.ring.free[rs]);
-      float cmx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      tmem_ld_wait();
+      if ((vm[0] & vm[1]) != 0xffffffffu) {  // some row is masked
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const int rr = 2 * i + par;
-        const float x =
-            ((vm[rr >> 5] >> (rr & 31)) & 1u) ? __uint_as_float(sv[i]) * P.scale2 : -INFINITY;
-        sv[i] = __float_as_uint(x);
-        cmx[i & 3] = fmaxf(cmx[i & 3], x);
+        for (int i = 0; i < 32; ++i) {
+          const int row = 8 * (i >> 2) + 2 * quad + (i & 1);
+          if (!((vm[row >> 5] >> (row & 31)) & 1u)) sv[i] = 0xff800000u;  // -inf
+        }
       }
-      float cm = fmaxf(fmaxf(cmx[0], cmx[1]), fmaxf(cmx[2], cmx[3]));
-      cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 2));
-      float al = 1.f;
-      if (cm > mu + kLazy || (mu == -INFINITY && cm != -INFINITY)) {
-        al = mu == -INFINITY ? 0.f : exp2f(mu - cm);
-        mu = cm;
+      float cm[2], al[2], mref[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(sv[4 * (i >> 1) + 2 * x + (i & 1)]));
+        cm[x] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
       }
-      lsum *= al;
-      if (par == 0) S.alpha[hh] = al;
-      if (reduce_softmax(al != 1.f && j > c0, false)) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) cm[x] = fmaxf(cm[x], __shfl_xor_sync(0xffffffffu, cm[x], 1));
+#pragma unroll
+      for (int x = 0; x < 2; ++x) cm[x] = fmaxf(cm[x], __shfl_xor_sync(0xffffffffu, cm[x], 2));
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        cm[x] *= P.scale2;
+        al[x] = 1.f;
+        if (cm[x] > mu[x] + kLazy || (mu[x] == -INFINITY && cm[x] != -INFINITY)) {
+          al[x] = mu[x] == -INFINITY ? 0.f : ex2(mu[x] - cm[x]);
+          mu[x] = cm[x];
+        }
+        lsum[x] *= al[x];
+        mref[x] = mu[x] == -INFINITY ? 0.f : mu[x];
+      }
+      if (reduce_softmax((al[0] != 1.f || al[1] != 1.f) && j > c0, false)) {
         // rare: scale O^T by alpha once the previous chunk's products are done
+        if (quad == 0) {
+          S.alpha[hq] = al[0];
+          S.alpha[hq + 8] = al[1];
+        }
         const int pi = it - 1;
         ok = reduce_softmax(mbar_wait(&S.kv_free[pi % kBuf], (uint32_t)(pi / kBuf) & 1, kErrSoftmax),
                             true);
@@ -323,52 +367,53 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
           tmem_st_x16(ta, o);
         }
         tmem_st_wait();
+        bar_softmax();  // alpha is read before the next chunk may write it
       }
+      // p = 2^(s * scale2 - m), paired into f16x2
+      float l4[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {  // i = 2 * (column group) + head
+        const int x = i & 1;
+        const float p0 = ex2(fmaf(__uint_as_float(sv[2 * i]), P.scale2, -mref[x]));
+        const float p1 = ex2(fmaf(__uint_as_float(sv[2 * i + 1]), P.scale2, -mref[x]));
+        l4[x][0] += p0;
+        l4[x][1] += p1;
+        sv[i] = pack2<kFp4>(p0, p1);
+      }
+      lsum[0] += l4[0][0] + l4[0][1];
+      lsum[1] += l4[1][0] + l4[1][1];
       // the P buffer was read by the products of chunk j - 2
       if (it >= kBuf) {
         const int pi = it - kBuf;
         ok = reduce_softmax(mbar_wait(&S.kv_free[slot], (uint32_t)(pi / kBuf) & 1, kErrSoftmax), true);
         if (!ok) break;
       }
-      // P row of this head into the K-major tile [head][64 rows]. Per 16 rows the even thread
-      // writes rows 0-7 and the odd one rows 8-15, after exchanging four values.
+      // K-major tile [head][64 rows]: 8 x 8 pieces of 16-bit values, four a store: column groups
+      // 2 c and 2 c + 1 of heads 16w .. 16w + 7 and 16w + 8 .. 16w + 15. Lane l gives the address
+      // of row l % 8 of piece l / 8 (heads + 8 in odd pieces).
       {
-        uint8_t* pt = base + kOffP + slot * kSlotP;
-        float lc[4] = {0.f, 0.f, 0.f, 0.f};  // sums of what the MMA multiplies
-        const float mref = mu == -INFINITY ? 0.f : mu;
+        const uint32_t pt = smem_u32(base + kOffP + slot * kSlotP);
+        const int head = 16 * warp + (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
-        for (int gr = 0; gr < kRows / 16; ++gr) {
-          uint32_t bb[8];
-#pragma unroll
-          for (int m = 0; m < 8; ++m) {
-            const __half hv = __float2half_rn(exp2f(__uint_as_float(sv[8 * gr + m]) - mref));
-            lc[m & 3] += __half2float(hv);
-            bb[m] = (uint32_t)__half_as_ushort(hv);
-          }
-          const uint32_t s0 = par ? (bb[0] | (bb[1] << 16)) : (bb[4] | (bb[5] << 16));
-          const uint32_t s1 = par ? (bb[2] | (bb[3] << 16)) : (bb[6] | (bb[7] << 16));
-          const uint32_t r0 = __shfl_xor_sync(0xffffffffu, s0, 2);
-          const uint32_t r1 = __shfl_xor_sync(0xffffffffu, s1, 2);
-          const uint32_t pk[4] = {r0 & 0xffffu, r0 >> 16, r1 & 0xffffu, r1 >> 16};
-          uint32_t w[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t own = par ? bb[4 + k] : bb[k];
-            w[k] = par ? (pk[k] | (own << 16)) : (own | (pk[k] << 16));
-          }
-          *reinterpret_cast<uint4*>(pt + sw128(hh, 2 * gr + par)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        lsum += (lc[0] + lc[1]) + (lc[2] + lc[3]);
+        for (int c = 0; c < 4; ++c)
+          stmatrix_x4(pt + sw128(head, 2 * c + (lane >> 4)), sv[4 * c], sv[4 * c + 1], sv[4 * c + 2],
+                      sv[4 * c + 3]);
       }
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.p_full[slot]);
     }
-    lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
-    if (par == 0) {
-      S.m_used[hh] = mu;
-      S.l_sum[hh] = lsum;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      lsum[x] += __shfl_xor_sync(0xffffffffu, lsum[x], 1);
+      lsum[x] += __shfl_xor_sync(0xffffffffu, lsum[x], 2);
+    }
+    if (quad == 0) {
+      S.m_used[hq] = mu[0];
+      S.m_used[hq + 8] = mu[1];
+      S.l_sum[hq] = lsum[0];
+      S.l_sum[hq + 8] = lsum[1];
     }
     // ---- epilogue ----
     if (ok && c1 > c0) {

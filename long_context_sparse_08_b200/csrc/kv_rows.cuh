@@ -245,6 +245,19 @@ __device__ __forceinline__ void store_atom(const Held& v, uint8_t* dst, bool cac
   }
 }
 
+// Whether the phase with the given parity has completed (no waiting).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // cos / sin of the query position for the 32 RoPE pairs.
 struct RopeTable {
   float cs[kR / 2], sn[kR / 2];
@@ -316,10 +329,10 @@ __device__ __forceinline__ float unpack_hi(uint32_t w) {
 }
 
 // The gather warps' loop over chunks [c0, c1): kBufs KV buffers of kAtoms atoms at `kv`, a full
-// barrier per (buffer, atom) and a free barrier per buffer, or per (buffer, atom) with
-// kAtomFree (a kernel that reads each atom once may give it back alone). Loads of a chunk are
+// and a free barrier per buffer (full: one arrival per warp), or with kPerAtom per (buffer,
+// atom), so that an atom is multiplied and given back by itself. Loads of a chunk are
 // issued before the wait for its buffer.
-template <int kFmt, int kBufs, bool kAtomFree>
+template <int kFmt, int kBufs, bool kPerAtom>
 __device__ __forceinline__ void gather_loop(uint8_t* kv, int c0, int c1, int nc, int atom,
                                             AddrRing& ring, uint64_t* full, uint64_t* free,
                                             int code) {
@@ -334,13 +347,13 @@ __device__ __forceinline__ void gather_loop(uint8_t* kv, int c0, int c1, int nc,
     load_atom<kFmt>(v, ring.src[rs], cache, atom);
     __syncwarp();
     if (lane == 0) mbar_arrive(&ring.free[rs]);
-    ok = __all_sync(0xffffffffu, mbar_wait(&free[kAtomFree ? slot * kAtoms + atom : slot],
+    ok = __all_sync(0xffffffffu, mbar_wait(&free[kPerAtom ? slot * kAtoms + atom : slot],
                                            ((uint32_t)(it / kBufs) & 1) ^ 1, code + 1));
     if (!ok) break;
     store_atom<kFmt>(v, kv + (size_t)(slot * kAtoms + atom) * kAtomBytes, cache, atom);
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&full[slot * kAtoms + atom]);
+    if (lane == 0) mbar_arrive(&full[kPerAtom ? slot * kAtoms + atom : slot]);
   }
 }
 
