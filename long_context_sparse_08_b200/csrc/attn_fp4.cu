@@ -221,73 +221,69 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
     resolve_rows<kFp4>(a, l, bt, b, c0, c1, S.ring, kErrRing);
   } else if (warp == 4) {
     // ------------------------------ MMA issuer ------------------------------
-    const uint32_t idS = idesc_f16(0, kHg, kRows);             // M = 64, N = 64, both K-major
-    const uint32_t idO = idesc_f16(0, 128, kHg) | (1u << 15);  // M = 128 dims; A MN-major
-    const uint64_t dq = smem_desc(smem_u32(base + kOffQ), 16, 1024, kLayoutSw128);
-    bool ok = c0 < c1 && __all_sync(0xffffffffu, mbar_wait(&S.q_full, 0, kErrMma));
-    // S runs at most one chunk ahead of O^T. Where both could be issued, whichever has its
-    // operands goes first, O^T before S (it frees a buffer). S tile slot j % 2 was read by the
-    // softmax of chunk j - 2 before it published P(j - 2), which this warp has waited for.
-    int js = c0, jv = c0;
-    long long t0 = clock64();  // of the last step
-    while (ok && jv < c1) {
-      const int iv = jv - c0, is = js - c0;
-      const bool can_v = jv < js, can_s = js < c1 && js - jv < kBuf;
-      uint64_t* const pb = &S.p_full[iv % kBuf];
-      uint64_t* const kb = &S.kv_full[is % kBuf];
-      const uint32_t pp = (uint32_t)(iv / kBuf) & 1, kp = (uint32_t)(is / kBuf) & 1;
-      bool do_v = can_v, do_s = can_s;
-      if (can_v && can_s) {
-        do_v = __any_sync(0xffffffffu, mbar_test(pb, pp));
-        do_s = !do_v && __any_sync(0xffffffffu, mbar_test(kb, kp));
-        if (!do_v && !do_s) {
-          if (clock64() - t0 > kSpinCycles) {
-            set_error(kErrMma);
-            ok = false;
+    // One thread runs the whole loop: a step of it (votes, branches) costs as much as its MMAs
+    // when the warp runs it together.
+    if (elect_one()) {
+      const uint32_t idS = idesc_f16(0, kHg, kRows);             // M = 64, N = 64, both K-major
+      const uint32_t idO = idesc_f16(0, 128, kHg) | (1u << 15);  // M = 128 dims; A MN-major
+      const uint32_t sb = smem_u32(base);
+      const uint64_t dq = smem_desc(sb + kOffQ, 16, 1024, kLayoutSw128);
+      const uint64_t dk0 = smem_desc(sb + kOffKV, 16, 1024, kLayoutSw128);
+      const uint64_t dv0 = smem_desc(sb + kOffKV, kAtomBytes, 1024, kLayoutSw128);
+      const uint64_t dp0 = smem_desc(sb + kOffP, 16, 1024, kLayoutSw128);
+      // S runs at most one chunk ahead of O^T. Where both could be issued, whichever has its
+      // operands goes first, O^T before S (it frees a buffer). S tile slot i % 2 was read by the
+      // softmax of chunk i - 2 before it published P(i - 2), which this thread has waited for.
+      const int n = c1 - c0;
+      int is = 0, iv = 0;
+      bool ok = n > 0 && mbar_wait(&S.q_full, 0, kErrMma);
+      while (ok && iv < n) {
+        const int ss = is & 1, sv = iv & 1;
+        const uint32_t kp = (uint32_t)(is >> 1) & 1, pp = (uint32_t)(iv >> 1) & 1;
+        bool do_v;
+        if (iv < is && is < n && is - iv < kBuf) {
+          const long long t0 = clock64();
+          while (true) {
+            do_v = mbar_test(&S.p_full[sv], pp);
+            if (do_v || mbar_test(&S.kv_full[ss], kp)) break;
+            if (clock64() - t0 > kSpinCycles) {
+              set_error(kErrMma);
+              ok = false;
+              break;
+            }
           }
-          ok = __all_sync(0xffffffffu, ok);
-          continue;
+        } else {
+          do_v = iv < is;
+          ok = mbar_wait(do_v ? &S.p_full[sv] : &S.kv_full[ss], do_v ? pp : kp, kErrMma);
         }
-      }
-      ok = __all_sync(0xffffffffu, mbar_wait(do_v ? pb : kb, do_v ? pp : kp, kErrMma));
-      if (!ok) break;
-      tc_fence_after();
-      if (do_v) {
-        const int slot = iv % kBuf;
-        const uint64_t dv = smem_desc(smem_u32(base + kOffKV + slot * kSlotKV), kAtomBytes, 1024,
-                                      kLayoutSw128);
-        const uint64_t dp = smem_desc(smem_u32(base + kOffP + slot * kSlotP), 16, 1024, kLayoutSw128);
-        if (elect_one()) {
+        if (!ok) break;
+        tc_fence_after();
+        if (do_v) {
+          const uint64_t dv = dv0 + (uint64_t)(sv * (kSlotKV >> 4)), dp = dp0 + (uint64_t)(sv * (kSlotP >> 4));
 #pragma unroll
           for (int kk = 0; kk < kRows / 16; ++kk)
 #pragma unroll
             for (int sl = 0; sl < 4; ++sl)
               mma_f16(tmem + kColO + 64 * sl, dv + ((sl * 2 * kAtomBytes + kk * 2048) >> 4),
-                      dp + ((kk * 32) >> 4), idO, (jv > c0 || kk > 0) ? 1u : 0u);
-          mma_commit(&S.kv_free[slot]);
-        }
-        ++jv;
-      } else {
-        const int slot = is % kBuf;
-        const uint64_t dk = smem_desc(smem_u32(base + kOffKV + slot * kSlotKV), 16, 1024, kLayoutSw128);
-        if (elect_one()) {
+                      dp + ((kk * 32) >> 4), idO, (iv > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&S.kv_free[sv]);
+          ++iv;
+        } else {
+          const uint64_t dk = dk0 + (uint64_t)(ss * (kSlotKV >> 4));
 #pragma unroll
           for (int atom = 0; atom < kAtoms; ++atom)
 #pragma unroll
             for (int kq = 0; kq < 4; ++kq)
-              mma_f16(tmem + kColS + 64 * slot, dq + ((atom * (kHg * 128) + kq * 32) >> 4),
+              mma_f16(tmem + kColS + 64 * ss, dq + ((atom * (kHg * 128) + kq * 32) >> 4),
                       dk + ((atom * kAtomBytes + kq * 32) >> 4), idS, (atom | kq) != 0 ? 1u : 0u);
-          mma_commit(&S.s_full[slot]);
+          mma_commit(&S.s_full[ss]);
+          ++is;
         }
-        ++js;
       }
-      __syncwarp();
-      t0 = clock64();
+      mma_commit(&S.done);  // fires when nothing issued here is in flight
+      mbar_wait(&S.done, 0, kErrMma);
     }
     __syncwarp();
-    if (elect_one()) mma_commit(&S.done);  // fires when nothing issued here is in flight
-    __syncwarp();
-    mbar_wait(&S.done, 0, kErrMma);
   } else {
     prepare_q<8>(a, bt, h0, 8 * warp, base + kOffQ, S.rope);
     __syncwarp();
