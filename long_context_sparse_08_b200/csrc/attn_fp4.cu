@@ -61,7 +61,9 @@ struct Smem {
   AddrRing ring;
   uint64_t kv_full[kBuf], kv_free[kBuf], s_full[kBuf], p_full[kBuf], q_full, done;
   uint32_t tmem_slot;
-  float m_used[kHg], l_sum[kHg], alpha[kHg], fin[kHg];
+  uint64_t vote[2];
+  uint32_t need[4][4];  // [chunk % 4][softmax warp]: a head of the warp raised its maximum
+  float m_used[kHg], l_sum[kHg], alpha[2][kHg], fin[kHg];
   RopeTable rope;
 };
 
@@ -76,19 +78,10 @@ struct Params {
 constexpr size_t kPartFloats = (size_t)kHg * (kC + 2);
 
 __device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool reduce_softmax(bool p, bool all) {
-  uint32_t res;
-  if (all)
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-        "bar.red.and.pred p, 1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(res) : "r"((uint32_t)p) : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-        "bar.red.or.pred p, 1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(res) : "r"((uint32_t)p) : "memory");
-  return res != 0;
+// A wait of one softmax warp. No barrier of the four warps follows it inside the chunk loop,
+// so a warp whose wait gives up leaves the others to their own limits.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, kErrSoftmax));
 }
 
 // 16 TMEM lanes x 64 columns of 32-bit as eight 16 x 8 pieces: thread t gets, in registers 4 i
@@ -140,33 +133,40 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// q_hat of heads first .. first + kN - 1 of the group, by one warp, all of them in flight.
-template <int kN>
-__device__ __forceinline__ void prepare_q(const MqaArgs& a, int bt, int h0, int first, uint8_t* qs,
-                                          const RopeTable& rope) {
+// q_hat of heads first .. first + n - 1 of the group, by one warp: two heads at a time, the
+// next two in flight. A rolled loop: this code runs once per CTA, and unrolled over the heads
+// fetching its instructions took longer than running them.
+__device__ __forceinline__ void prepare_q(const MqaArgs& a, int bt, int h0, int first, int n,
+                                          uint8_t* qs, const RopeTable& rope) {
   const int lane = threadIdx.x & 31;
   const uint4* qg = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                   ((size_t)bt * a.H + h0 + first) * kC);
-  uint4 raw[kN][2];
+                                                   ((size_t)bt * a.H + h0 + first) * kC) + lane;
+  uint4 raw[2][2], next[2][2];
 #pragma unroll
-  for (int i = 0; i < kN; ++i)
-#pragma unroll
-    for (int half = 0; half < 2; ++half)
-      raw[i][half] = __ldg(qg + (size_t)i * (kC / 8) + 32 * half + lane);
+  for (int i = 0; i < 4; ++i) next[i >> 1][i & 1] = __ldg(qg + 32 * i);
   float w[16];
   qhat_weights(a.q_rms_w, w);
+#pragma unroll 1
+  for (int h = 0; h < n; h += 2) {
 #pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    float y[16];
-    qhat_lane(raw[i], w, a.eps, rope, y);
+    for (int i = 0; i < 4; ++i) raw[i >> 1][i & 1] = next[i >> 1][i & 1];
+    if (h + 2 < n) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint32_t o[4];
+      for (int i = 0; i < 4; ++i) next[i >> 1][i & 1] = __ldg(qg + (size_t)(h + 2) * (kC / 8) + 32 * i);
+    }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] = pack2<kFp4>(y[8 * half + 2 * k], y[8 * half + 2 * k + 1]);
-      const int c = lane + 32 * half;  // 16-byte piece of the row
-      *reinterpret_cast<uint4*>(qs + (c >> 3) * (kHg * 128) + sw128(first + i, c & 7)) =
-          make_uint4(o[0], o[1], o[2], o[3]);
+    for (int i = 0; i < 2; ++i) {
+      float y[16];
+      qhat_lane(raw[i], w, a.eps, rope, y);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = pack2<kFp4>(y[8 * half + 2 * k], y[8 * half + 2 * k + 1]);
+        const int c = lane + 32 * half;  // 16-byte piece of the row
+        *reinterpret_cast<uint4*>(qs + (c >> 3) * (kHg * 128) + sw128(first + h + i, c & 7)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+      }
     }
   }
   fence_proxy_async_smem();
@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
         mbar_init(&S.kv_free[i], 1);
         mbar_init(&S.s_full[i], 1);
         mbar_init(&S.p_full[i], 4);
+        mbar_init(&S.vote[i], 4);
       }
       mbar_init(&S.q_full, 12);  // softmax and gather warps
       mbar_init(&S.done, 1);
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
   const uint32_t tmem = S.tmem_slot;
 
   if (warp >= 6) {
-    prepare_q<4>(a, bt, h0, 32 + 4 * (warp - 6), base + kOffQ, S.rope);
+    prepare_q(a, bt, h0, 32 + 4 * (warp - 6), 4, base + kOffQ, S.rope);
     __syncwarp();
     if (lane == 0) mbar_arrive(&S.q_full);
     gather_loop<kFp4, kBuf, false>(base + kOffKV, c0, c1, l.nc, warp - 6, S.ring, S.kv_full,
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
     }
     __syncwarp();
   } else {
-    prepare_q<8>(a, bt, h0, 8 * warp, base + kOffQ, S.rope);
+    prepare_q(a, bt, h0, 8 * warp, 8, base + kOffQ, S.rope);
     __syncwarp();
     if (lane == 0) mbar_arrive(&S.q_full);
     // ------------------------------ softmax ------------------------------
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
 #pragma unroll 1
     for (int j = c0; j < c1 && ok; ++j) {
       const int it = j - c0, slot = it % kBuf, rs = it % kRing;
-      ok = reduce_softmax(mbar_wait(&S.s_full[slot], (uint32_t)(it / kBuf) & 1, kErrSoftmax), true);
+      ok = wait_warp(&S.s_full[slot], (uint32_t)(it / kBuf) & 1);
       if (!ok) break;
       tc_fence_after();
       uint32_t sv[32];
@@ -340,31 +341,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
         lsum[x] *= al[x];
         mref[x] = mu[x] == -INFINITY ? 0.f : mu[x];
       }
-      if (reduce_softmax((al[0] != 1.f || al[1] != 1.f) && j > c0, false)) {
-        // rare: scale O^T by alpha once the previous chunk's products are done
-        if (quad == 0) {
-          S.alpha[hq] = al[0];
-          S.alpha[hq + 8] = al[1];
-        }
-        const int pi = it - 1;
-        ok = reduce_softmax(mbar_wait(&S.kv_free[pi % kBuf], (uint32_t)(pi / kBuf) & 1, kErrSoftmax),
-                            true);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll 1
-        for (int cg = 0; cg < 16; ++cg) {  // 4 slices x 4 groups of 16 heads
-          uint32_t o[16];
-          const uint32_t ta = lane_base + kColO + 16 * cg;
-          tmem_ld_x16(ta, o);
-          tmem_ld_wait();
-#pragma unroll
-          for (int h = 0; h < 16; ++h)
-            o[h] = __float_as_uint(__uint_as_float(o[h]) * S.alpha[16 * (cg & 3) + h]);
-          tmem_st_x16(ta, o);
-        }
-        tmem_st_wait();
-        bar_softmax();  // alpha is read before the next chunk may write it
+      // the warps tell one another whether a maximum was raised, and look once P is computed
+      const bool raised = __any_sync(0xffffffffu, (al[0] != 1.f || al[1] != 1.f) && j > c0);
+      if (quad == 0) {
+        S.alpha[it & 1][hq] = al[0];
+        S.alpha[it & 1][hq + 8] = al[1];
       }
+      if (lane == 0) S.need[it & 3][warp] = raised ? 1u : 0u;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.vote[it & 1]);
       // p = 2^(s * scale2 - m), paired into f16x2
       float l4[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
@@ -378,10 +363,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
       }
       lsum[0] += l4[0][0] + l4[0][1];
       lsum[1] += l4[1][0] + l4[1][1];
-      // the P buffer was read by the products of chunk j - 2
-      if (it >= kBuf) {
-        const int pi = it - kBuf;
-        ok = reduce_softmax(mbar_wait(&S.kv_free[slot], (uint32_t)(pi / kBuf) & 1, kErrSoftmax), true);
+      ok = wait_warp(&S.vote[it & 1], (uint32_t)(it >> 1) & 1);
+      if (!ok) break;
+      if ((S.need[it & 3][0] | S.need[it & 3][1] | S.need[it & 3][2] | S.need[it & 3][3]) != 0) {
+        // rare: scale this warp's dims of O^T by alpha once the previous chunk's products are
+        // done (a chunk's alpha is rewritten two chunks later, after all warps published P)
+        const int pi = it - 1;
+        ok = wait_warp(&S.kv_free[pi % kBuf], (uint32_t)(pi / kBuf) & 1);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int cg = 0; cg < 16; ++cg) {  // 4 slices x 4 groups of 16 heads
+          uint32_t o[16];
+          const uint32_t ta = lane_base + kColO + 16 * cg;
+          tmem_ld_x16(ta, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int h = 0; h < 16; ++h)
+            o[h] = __float_as_uint(__uint_as_float(o[h]) * S.alpha[it & 1][16 * (cg & 3) + h]);
+          tmem_st_x16(ta, o);
+        }
+        tmem_st_wait();
+      }
+      if (it >= kBuf) {  // the P buffer was read by the products of chunk j - 2
+        ok = wait_warp(&S.kv_free[slot], (uint32_t)((it - kBuf) / kBuf) & 1);
         if (!ok) break;
       }
       // K-major tile [head][64 rows]: 8 x 8 pieces of 16-bit values, four a store: column groups
@@ -414,8 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
     // ---- epilogue ----
     if (ok && c1 > c0) {
       const int last = c1 - c0 - 1;
-      ok = reduce_softmax(
-          mbar_wait(&S.kv_free[last % kBuf], (uint32_t)(last / kBuf) & 1, kErrSoftmax), true);
+      ok = wait_warp(&S.kv_free[last % kBuf], (uint32_t)(last / kBuf) & 1);
     }
     bar_softmax();
     const bool single = P.nsplit == 1;
@@ -491,24 +495,36 @@ __global__ void __launch_bounds__(256) k_attn_fp4_combine(const __grid_constant_
   const int64_t t = a.q_pos[bt];
   const int d = 2 * threadIdx.x, ns = P.nsplit;
   const float* base = P.part + (size_t)stream * ns * kPartFloats;
-  float ms[kMaxSplit], M = -INFINITY;
+  // every load of eight splits goes out before any is used
+  float M = -INFINITY;
+  for (int s0 = 0; s0 < ns; s0 += 8) {
+    float ms[8];
 #pragma unroll
-  for (int s = 0; s < kMaxSplit; ++s) {
-    ms[s] = s < ns ? base[s * kPartFloats + h] : -INFINITY;
-    M = fmaxf(M, ms[s]);
+    for (int s = 0; s < 8; ++s) ms[s] = s0 + s < ns ? base[(s0 + s) * kPartFloats + h] : -INFINITY;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) M = fmaxf(M, ms[s]);
   }
   const float zs = a.sink ? a.sink[g * kHg + h] * 1.44269504088896341f : -INFINITY;
   M = fmaxf(M, zs);
   float l = 0.f, o0 = 0.f, o1 = 0.f;
+  for (int s0 = 0; s0 < ns; s0 += 8) {
+    float ms[8], ls[8];
+    float2 os[8];
 #pragma unroll
-  for (int s = 0; s < kMaxSplit; ++s) {
-    if (ms[s] != -INFINITY) {
-      const float f = exp2f(ms[s] - M);
-      const float* pp = base + s * kPartFloats;
-      l = fmaf(pp[kHg + h], f, l);
-      const float2 o = *reinterpret_cast<const float2*>(pp + 2 * kHg + (size_t)h * kC + d);
-      o0 = fmaf(o.x, f, o0);
-      o1 = fmaf(o.y, f, o1);
+    for (int s = 0; s < 8; ++s) {
+      const float* pp = base + (size_t)min(s0 + s, ns - 1) * kPartFloats;
+      ms[s] = s0 + s < ns ? pp[h] : -INFINITY;
+      ls[s] = pp[kHg + h];
+      os[s] = *reinterpret_cast<const float2*>(pp + 2 * kHg + (size_t)h * kC + d);
+    }
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      if (ms[s] != -INFINITY) {
+        const float f = exp2f(ms[s] - M);
+        l = fmaf(ls[s], f, l);
+        o0 = fmaf(os[s].x, f, o0);
+        o1 = fmaf(os[s].y, f, o1);
+      }
     }
   }
   float y0 = 0.f, y1 = 0.f;
