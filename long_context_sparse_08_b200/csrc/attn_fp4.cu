@@ -14,9 +14,9 @@
 //   S[64 heads x 64 rows] = q_hat . K^T          (M = 64; A = q_hat, B = the KV tile)
 //   P = 2^(S * scale * log2(e) - m_h) in f16     (four threads a head)
 //   O^T[4 x 128 dims x 64 heads] += V^T . P^T    (A = the same KV tile read MN-major)
-// Warps: 0-3 softmax and epilogue; 4 issues the MMAs; 5 resolves addresses; 6-13 each widen
-// one 64-value atom of every row (kv_rows.cuh); 0-3 and 6-13 prepare q_hat first. Two KV
-// buffers: S of chunk j + 1 may be issued before O^T of chunk j, so the tensor cores work
+// q_hat comes as a prepared tile (q_tiles.cu). Warps: 0-3 softmax and epilogue; 4 issues the
+// MMAs; 5 resolves addresses; 6-13 each widen one 64-value atom of every row (kv_rows.cuh). Two
+// KV buffers: S of chunk j + 1 may be issued before O^T of chunk j, so the tensor cores work
 // during the softmax, and the gather warps fill the buffer that O^T released.
 // The running max m_h is raised only when a chunk's max exceeds it by more than 2^11.5 (then
 // O^T and l are rescaled); P stays below 2^11.5, inside f16, and sums are fp32.
@@ -64,15 +64,16 @@ struct Smem {
   uint64_t vote[2];
   uint32_t need[4][4];  // [chunk % 4][softmax warp]: a head of the warp raised its maximum
   float m_used[kHg], l_sum[kHg], alpha[2][kHg], fin[kHg];
-  RopeTable rope;
+  float2 rope[kR / 2];  // cos, sin of the query's position
 };
 
 struct Params {
   MqaArgs a;
   int G, nsplit;
   float* part;  // [stream][split][64 m | 64 l | 64 x 512 O], or nullptr
-  float scale2; // scale * log2(e)
-  double inv_freq[kR / 2];
+  const uint8_t* tiles;  // q_hat tiles, 64 KB per stream
+  const float2* rope;    // [B * T][32]
+  float scale2;          // scale * log2(e)
 };
 
 constexpr size_t kPartFloats = (size_t)kHg * (kC + 2);
@@ -133,45 +134,6 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// q_hat of heads first .. first + n - 1 of the group, by one warp: two heads at a time, the
-// next two in flight. A rolled loop: this code runs once per CTA, and unrolled over the heads
-// fetching its instructions took longer than running them.
-__device__ __forceinline__ void prepare_q(const MqaArgs& a, int bt, int h0, int first, int n,
-                                          uint8_t* qs, const RopeTable& rope) {
-  const int lane = threadIdx.x & 31;
-  const uint4* qg = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                   ((size_t)bt * a.H + h0 + first) * kC) + lane;
-  uint4 raw[2][2], next[2][2];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) next[i >> 1][i & 1] = __ldg(qg + 32 * i);
-  float w[16];
-  qhat_weights(a.q_rms_w, w);
-#pragma unroll 1
-  for (int h = 0; h < n; h += 2) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) raw[i >> 1][i & 1] = next[i >> 1][i & 1];
-    if (h + 2 < n) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) next[i >> 1][i & 1] = __ldg(qg + (size_t)(h + 2) * (kC / 8) + 32 * i);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float y[16];
-      qhat_lane(raw[i], w, a.eps, rope, y);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t o[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = pack2<kFp4>(y[8 * half + 2 * k], y[8 * half + 2 * k + 1]);
-        const int c = lane + 32 * half;  // 16-byte piece of the row
-        *reinterpret_cast<uint4*>(qs + (c >> 3) * (kHg * 128) + sw128(first + h + i, c & 7)) =
-            make_uint4(o[0], o[1], o[2], o[3]);
-      }
-    }
-  }
-  fence_proxy_async_smem();
-}
-
 __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant__ Params P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_align1024(smem_raw);
@@ -194,18 +156,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
         mbar_init(&S.p_full[i], 4);
         mbar_init(&S.vote[i], 4);
       }
-      mbar_init(&S.q_full, 12);  // softmax and gather warps
+      mbar_init(&S.q_full, 1);
       mbar_init(&S.done, 1);
       fence_barrier_init();
     }
     __syncwarp();
     tmem_alloc(&S.tmem_slot, kTmemCols);
   }
-  pdl_wait();  // positions, lists and queries may belong to the previous kernels
+  // The q_tiles launch before this one waited for everything earlier on the stream, and this
+  // kernel starts after that: only the tiles themselves are waited for, below.
   const List l = make_list(a, bt);
   const int c0 = (int)(((int64_t)l.n_chunks * split) / P.nsplit);
   const int c1 = (int)(((int64_t)l.n_chunks * (split + 1)) / P.nsplit);
-  if (warp == 0) rope_angle_cs((double)l.t, P.inv_freq[lane], &S.rope.cs[lane], &S.rope.sn[lane]);
+  RowBatch rows0;
+  if (warp == 5) rows0.lookup(a, l, bt, b, c0, c1);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -213,13 +177,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
   const uint32_t tmem = S.tmem_slot;
 
   if (warp >= 6) {
-    prepare_q(a, bt, h0, 32 + 4 * (warp - 6), 4, base + kOffQ, S.rope);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&S.q_full);
     gather_loop<kFp4, kBuf, false>(base + kOffKV, c0, c1, l.nc, warp - 6, S.ring, S.kv_full,
                                    S.kv_free, kErrGather);
   } else if (warp == 5) {
-    resolve_rows<kFp4>(a, l, bt, b, c0, c1, S.ring, kErrRing);
+    resolve_rows<kFp4>(rows0, a, l, bt, b, c0, c1, S.ring, kErrRing);
   } else if (warp == 4) {
     // ------------------------------ MMA issuer ------------------------------
     // One thread runs the whole loop: a step of it (votes, branches) costs as much as its MMAs
@@ -237,7 +198,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
       // softmax of chunk i - 2 before it published P(i - 2), which this thread has waited for.
       const int n = c1 - c0;
       int is = 0, iv = 0;
-      bool ok = n > 0 && mbar_wait(&S.q_full, 0, kErrMma);
+      bool ok = n > 0;
+      if (ok) {
+        pdl_wait();  // the tiles
+        mbar_arrive_expect_tx(&S.q_full, kAtoms * kHg * 128);
+        bulk_load(base + kOffQ, P.tiles + (size_t)stream * (kAtoms * kHg * 128), kAtoms * kHg * 128,
+                  &S.q_full);
+        ok = mbar_wait(&S.q_full, 0, kErrMma);
+      }
       while (ok && iv < n) {
         const int ss = is & 1, sv = iv & 1;
         const uint32_t kp = (uint32_t)(is >> 1) & 1, pp = (uint32_t)(iv >> 1) & 1;
@@ -286,9 +254,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
     }
     __syncwarp();
   } else {
-    prepare_q(a, bt, h0, 8 * warp, 8, base + kOffQ, S.rope);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&S.q_full);
     // ------------------------------ softmax ------------------------------
     const uint32_t lane_base = tmem + ((uint32_t)(32 * warp) << 16);
     // The M = 64 accumulator puts head 16w + i in TMEM lane 32w + i (i < 16). Four threads (a
@@ -417,6 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
       S.l_sum[hq + 8] = lsum[1];
     }
     // ---- epilogue ----
+    pdl_wait();  // the rotation, written beside the tiles
+    if (tid < kR / 2) S.rope[tid] = P.rope[(size_t)bt * 32 + tid];
     if (ok && c1 > c0) {
       const int last = c1 - c0 - 1;
       ok = wait_warp(&S.kv_free[last % kBuf], (uint32_t)(last / kBuf) & 1);
@@ -429,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
       if (single) {
         const float zs = a.sink ? a.sink[h0 + tid] * 1.44269504088896341f : -INFINITY;
         float f = 0.f;
-        if (lv > 0.f) {
+        if (lv != 0.f) {  // a NaN stays one
           const float M = fmaxf(m, zs);
           const float e = exp2f(m - M);
           f = e / (lv * e + (zs == -INFINITY ? 0.f : exp2f(zs - M)));
@@ -460,8 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
         float cs = 1.f, sn = 0.f;
         const bool rot = d >= kNope;
         if (rot) {
-          cs = S.rope.cs[(d - kNope) >> 1];
-          sn = -S.rope.sn[(d - kNope) >> 1];  // rotation by -t
+          cs = S.rope[(d - kNope) >> 1].x;
+          sn = -S.rope[(d - kNope) >> 1].y;  // rotation by -t
         }
 #pragma unroll
         for (int h = 0; h < 64; ++h) {
@@ -485,41 +452,44 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
   }
 }
 
-// Merge the partials of one head (fixed split order), add the sink, rotate by -t.
+// Merge the partials of one head (fixed split order), add the sink, rotate by -t. kBatch splits
+// are loaded before any is used.
+template <int kBatch>
 __global__ void __launch_bounds__(256) k_attn_fp4_combine(const __grid_constant__ Params P) {
-  pdl_wait();
-  pdl_trigger();
   const MqaArgs& a = P.a;
   const int stream = blockIdx.x, h = blockIdx.y;
   const int bt = stream / P.G, g = stream % P.G;
-  const int64_t t = a.q_pos[bt];
   const int d = 2 * threadIdx.x, ns = P.nsplit;
   const float* base = P.part + (size_t)stream * ns * kPartFloats;
-  // every load of eight splits goes out before any is used
-  float M = -INFINITY;
-  for (int s0 = 0; s0 < ns; s0 += 8) {
-    float ms[8];
-#pragma unroll
-    for (int s = 0; s < 8; ++s) ms[s] = s0 + s < ns ? base[(s0 + s) * kPartFloats + h] : -INFINITY;
-#pragma unroll
-    for (int s = 0; s < 8; ++s) M = fmaxf(M, ms[s]);
-  }
+  pdl_wait();
+  pdl_trigger();
   const float zs = a.sink ? a.sink[g * kHg + h] * 1.44269504088896341f : -INFINITY;
-  M = fmaxf(M, zs);
-  float l = 0.f, o0 = 0.f, o1 = 0.f;
-  for (int s0 = 0; s0 < ns; s0 += 8) {
-    float ms[8], ls[8];
-    float2 os[8];
+  float2 cs_sn = make_float2(1.f, 0.f);  // of +t
+  float M = zs, l = 0.f, o0 = 0.f, o1 = 0.f;
+  for (int s0 = 0; s0 < ns; s0 += kBatch) {
+    float ms[kBatch], ls[kBatch];
+    float2 os[kBatch];
 #pragma unroll
-    for (int s = 0; s < 8; ++s) {
+    for (int s = 0; s < kBatch; ++s) {
       const float* pp = base + (size_t)min(s0 + s, ns - 1) * kPartFloats;
-      ms[s] = s0 + s < ns ? pp[h] : -INFINITY;
+      ms[s] = pp[h];
       ls[s] = pp[kHg + h];
       os[s] = *reinterpret_cast<const float2*>(pp + 2 * kHg + (size_t)h * kC + d);
     }
+    if (s0 == 0 && d >= kNope) cs_sn = P.rope[(size_t)bt * 32 + ((d - kNope) >> 1)];
+    float Mn = M;
 #pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      if (ms[s] != -INFINITY) {
+    for (int s = 0; s < kBatch; ++s)
+      if (s0 + s < ns) Mn = fmaxf(Mn, ms[s]);
+    if (Mn == -INFINITY) continue;  // no row and no sink so far
+    const float f0 = exp2f(M - Mn);
+    l *= f0;
+    o0 *= f0;
+    o1 *= f0;
+    M = Mn;
+#pragma unroll
+    for (int s = 0; s < kBatch; ++s) {
+      if (s0 + s < ns && ms[s] != -INFINITY) {
         const float f = exp2f(ms[s] - M);
         l = fmaf(ls[s], f, l);
         o0 = fmaf(os[s].x, f, o0);
@@ -528,15 +498,13 @@ __global__ void __launch_bounds__(256) k_attn_fp4_combine(const __grid_constant_
     }
   }
   float y0 = 0.f, y1 = 0.f;
-  if (l > 0.f) {
+  if (l != 0.f) {  // a NaN stays one
     const float den = l + (zs == -INFINITY ? 0.f : exp2f(zs - M));
     y0 = o0 / den;
     y1 = o1 / den;
   }
   if (d >= kNope) {
-    float cs, sn;
-    rope_angle_cs(-(double)t, P.inv_freq[(d - kNope) >> 1], &cs, &sn);
-    const float u0 = y0 * cs - y1 * sn, u1 = y0 * sn + y1 * cs;
+    const float u0 = y0 * cs_sn.x + y1 * cs_sn.y, u1 = y1 * cs_sn.x - y0 * cs_sn.y;
     y0 = u0;
     y1 = u1;
   }
@@ -564,8 +532,8 @@ bool attn_fp4_supported(const MqaArgs& a) {
 
 size_t attn_fp4_workspace_bytes(const MqaArgs& a) {
   const int ns = choose_split(a);
-  if (ns <= 1) return 0;
-  return (size_t)a.B * a.T * (a.H / kHg) * ns * kPartFloats * sizeof(float);
+  const size_t part = ns <= 1 ? 0 : (size_t)a.B * a.T * (a.H / kHg) * ns * kPartFloats * sizeof(float);
+  return q_tiles_bytes(a, false) + q_rope_bytes(a) + part;
 }
 
 cudaError_t launch_attn_fp4(const MqaArgs& a, void* ws, size_t ws_bytes, cudaStream_t st) {
@@ -573,19 +541,25 @@ cudaError_t launch_attn_fp4(const MqaArgs& a, void* ws, size_t ws_bytes, cudaStr
   P.a = a;
   P.G = a.H / kHg;
   P.nsplit = choose_split(a);
-  P.part = P.nsplit > 1 ? static_cast<float*>(ws) : nullptr;
+  if (ws_bytes < attn_fp4_workspace_bytes(a)) return cudaErrorInvalidValue;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  P.tiles = w;
+  P.rope = reinterpret_cast<float2*>(w + q_tiles_bytes(a, false));
+  P.part = P.nsplit > 1
+               ? reinterpret_cast<float*>(w + q_tiles_bytes(a, false) + q_rope_bytes(a))
+               : nullptr;
   P.scale2 = a.scale * 1.44269504088896341f;
-  for (int p = 0; p < kR / 2; ++p) P.inv_freq[p] = rope_inv_freq(p, kR, (double)a.rope_base);
-  if (P.nsplit > 1 && ws_bytes < attn_fp4_workspace_bytes(a)) return cudaErrorInvalidValue;
   const int64_t streams = (int64_t)a.B * a.T * P.G;
   const size_t smem = 1024 + kOffEnd + sizeof(Smem);
   cudaError_t e = cudaFuncSetAttribute(k_attn_fp4, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
   if (e != cudaSuccess) return e;
-  e = launch(a.chained, k_attn_fp4, dim3((unsigned)(streams * P.nsplit)), dim3(kThreads), smem, st,
-             P);
+  e = launch_q_tiles(a, false, w, w + q_tiles_bytes(a, false), st);
+  if (e != cudaSuccess) return e;
+  e = launch(true, k_attn_fp4, dim3((unsigned)(streams * P.nsplit)), dim3(kThreads), smem, st, P);
   if (e != cudaSuccess || P.nsplit == 1) return e;
-  return launch(true, k_attn_fp4_combine, dim3((unsigned)streams, kHg), dim3(256), 0, st, P);
+  return launch(true, P.nsplit <= 8 ? k_attn_fp4_combine<8> : k_attn_fp4_combine<16>,
+                dim3((unsigned)streams, kHg), dim3(256), 0, st, P);
 }
 
 cudaError_t attn_fp4_device_error(int* code) {

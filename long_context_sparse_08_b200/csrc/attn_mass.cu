@@ -12,6 +12,7 @@
 //   [hi; lo][128 x 512] . K^T[512 x 64 rows] -> TMEM, z = (hi + lo) * scale * log2(e)
 // Head 16 w + i has hi in row 32 w + i and lo in row 32 w + 16 + i, so that both lie in the
 // TMEM lanes of one warp and one exchange adds them.
+//   q_tiles.cu      prepares the [hi; lo] tiles;
 //   k_mass_logits   (a CTA per (query, 64 heads, split)) writes z as fp32 and, per split and
 //                   head, the running maximum and sum;
 //   k_mass_dense    adds 2^(z - L) over queries and heads for one entry per thread;
@@ -54,7 +55,6 @@ struct Smem {
   AddrRing ring;
   uint64_t kv_full[kAtoms], kv_free[kAtoms], s_full[2], s_free[2], q_full, done;
   uint32_t tmem_slot;
-  RopeTable rope;
 };
 
 struct Params {
@@ -65,8 +65,8 @@ struct Params {
   float* part;               // [stream][split][m 64 | l 64]
   unsigned long long* fixed; // [B][n_cap] (sparse)
   float* acc;
+  const uint8_t* tiles;      // q_hat tiles, 128 KB per stream
   float scale2, decay;
-  double inv_freq[kR / 2];
 };
 
 template <int kFmt>
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mass_logits(const __grid_consta
         mbar_init(&S.s_full[i], 1);
         mbar_init(&S.s_free[i], 4);
       }
-      mbar_init(&S.q_full, 4);
+      mbar_init(&S.q_full, 1);
       mbar_init(&S.done, 1);
       fence_barrier_init();
     }
@@ -103,7 +103,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_mass_logits(const __grid_consta
   const List l = make_list(a, bt);
   const int c0 = (int)(((int64_t)l.n_chunks * split) / P.nsplit);
   const int c1 = (int)(((int64_t)l.n_chunks * (split + 1)) / P.nsplit);
-  if (warp == 0) rope_angle_cs((double)l.t, P.inv_freq[lane], &S.rope.cs[lane], &S.rope.sn[lane]);
+  RowBatch rows0;
+  if (warp == 5) rows0.lookup(a, l, bt, b, c0, c1);
   if (P.fixed != nullptr) {  // the sparse sums start at zero
     const size_t n = (size_t)a.B * a.n_cap, step = (size_t)gridDim.x * kThreads;
     for (size_t i = (size_t)blockIdx.x * kThreads + tid; i < n; i += step) P.fixed[i] = 0;
@@ -118,12 +119,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_mass_logits(const __grid_consta
     gather_loop<kFmt, 1, true>(base + kOffKV, c0, c1, l.nc, warp - 6, S.ring, S.kv_full, S.kv_free,
                                kErrGather);
   } else if (warp == 5) {
-    resolve_rows<kFmt>(a, l, bt, b, c0, c1, S.ring, kErrRing);
+    resolve_rows<kFmt>(rows0, a, l, bt, b, c0, c1, S.ring, kErrRing);
   } else if (warp == 4) {
     const uint32_t idS = idesc_f16(kFmt == kFp4 ? 0 : 1, kQRows, kRows);
     const uint64_t dq = smem_desc(smem_u32(base + kOffQ), 16, 1024, kLayoutSw128);
     const uint64_t dk = smem_desc(smem_u32(base + kOffKV), 16, 1024, kLayoutSw128);
-    bool ok = c0 < c1 && __all_sync(0xffffffffu, mbar_wait(&S.q_full, 0, kErrMma));
+    bool ok = c0 < c1;
+    if (ok) {
+      pdl_wait();  // the q_hat tiles of the launch before
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&S.q_full, kAtoms * kQAtom);
+        bulk_load(base + kOffQ, P.tiles + (size_t)stream * (kAtoms * kQAtom), kAtoms * kQAtom, &S.q_full);
+      }
+      __syncwarp();
+      ok = __all_sync(0xffffffffu, mbar_wait(&S.q_full, 0, kErrMma));
+    }
     for (int j = c0; j < c1 && ok; ++j) {
       const int it = j - c0, slot = it & 1;
       ok = __all_sync(0xffffffffu,
@@ -151,47 +161,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_mass_logits(const __grid_consta
     __syncwarp();
     mbar_wait(&S.done, 0, kErrMma);
   } else {
-    // ---- q_hat = hi + lo, a warp per head, eight heads in flight ----
-    {
-      float w[16];
-      qhat_weights(a.q_rms_w, w);
-      const uint4* qg = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                       ((size_t)bt * a.H + h0) * kC);
-      uint8_t* qs = base + kOffQ;
-#pragma unroll 1
-      for (int hb = 0; hb < 16; hb += 8) {
-        uint4 raw[8][2];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
-            raw[i][half] = __ldg(qg + (size_t)(16 * warp + hb + i) * (kC / 8) + 32 * half + lane);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = 32 * warp + hb + i;
-          float y[16];
-          qhat_lane(raw[i], w, a.eps, S.rope, y);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float u = y[8 * half + 2 * k], v = y[8 * half + 2 * k + 1];
-              hi[k] = pack2<kFmt>(u, v);
-              lo[k] = pack2<kFmt>(u - unpack_lo<kFmt>(hi[k]), v - unpack_hi<kFmt>(hi[k]));
-            }
-            const int c = lane + 32 * half;
-            uint8_t* at = qs + (c >> 3) * kQAtom;
-            *reinterpret_cast<uint4*>(at + sw128(row, c & 7)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(at + sw128(row + 16, c & 7)) =
-                make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.q_full);
-    }
     // ---- logits: lane i and i + 16 hold hi and lo of head 16 w + i % 16; after the exchange
     //      lane i has the head's rows 0-31 of the chunk and lane i + 16 its rows 32-63 ----
     const uint32_t lane_base = tmem + ((uint32_t)(32 * warp) << 16);
@@ -346,7 +315,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 struct Plan {
   int nsplit;
   int64_t z_rows;
-  size_t z_bytes, part_bytes, fixed_bytes;
+  size_t z_bytes, part_bytes, fixed_bytes, tile_bytes, rope_bytes;
 };
 
 Plan make_plan(const MqaArgs& a) {
@@ -356,6 +325,8 @@ Plan make_plan(const MqaArgs& a) {
   p.z_rows = ((a.k > 0 ? a.k : a.n_cap) + kRows - 1) / kRows * kRows;
   p.z_bytes = up256(streams * kHg * (size_t)p.z_rows * sizeof(float));
   p.part_bytes = up256(streams * p.nsplit * 2 * kHg * sizeof(float));
+  p.tile_bytes = q_tiles_bytes(a, true);
+  p.rope_bytes = q_rope_bytes(a);
   p.fixed_bytes = a.k > 0 ? up256((size_t)a.B * a.n_cap * 8) : 0;
   return p;
 }
@@ -364,7 +335,7 @@ Plan make_plan(const MqaArgs& a) {
 
 size_t attn_mass_workspace_bytes(const MqaArgs& a) {
   const Plan p = make_plan(a);
-  return p.z_bytes + p.part_bytes + p.fixed_bytes;
+  return p.z_bytes + p.part_bytes + p.fixed_bytes + p.tile_bytes + p.rope_bytes;
 }
 
 cudaError_t launch_attn_mass(const MqaArgs& a, float decay, float* acc, void* ws,
@@ -382,13 +353,16 @@ cudaError_t launch_attn_mass(const MqaArgs& a, float decay, float* acc, void* ws
   P.acc = acc;
   P.scale2 = a.scale * 1.44269504088896341f;
   P.decay = decay;
-  for (int p = 0; p < kR / 2; ++p) P.inv_freq[p] = rope_inv_freq(p, kR, (double)a.rope_base);
+  char* tiles = w + pl.z_bytes + pl.part_bytes + pl.fixed_bytes;
+  P.tiles = reinterpret_cast<const uint8_t*>(tiles);
   const int64_t streams = (int64_t)a.B * a.T * P.G;
   auto kern = a.fp4 ? k_mass_logits<kFp4> : k_mass_logits<kBf16>;
   const size_t smem = 1024 + kOffEnd + sizeof(Smem);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  e = launch(false, kern, dim3((unsigned)(streams * P.nsplit)), dim3(kThreads), smem, st, P);
+  e = launch_q_tiles(a, true, tiles, tiles + pl.tile_bytes, st);
+  if (e != cudaSuccess) return e;
+  e = launch(true, kern, dim3((unsigned)(streams * P.nsplit)), dim3(kThreads), smem, st, P);
   if (e != cudaSuccess) return e;
   const size_t lsm = (size_t)a.H * sizeof(float);
   if (a.k == 0)

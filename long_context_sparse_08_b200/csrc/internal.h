@@ -171,6 +171,11 @@ size_t mqa_tc_workspace_bytes(const MqaArgs& a);
 cudaError_t launch_zero(void* p0, size_t b0, void* p1, size_t b1, cudaStream_t st);
 cudaError_t launch_mqa_tc(const MqaArgs& a, void* ws, size_t ws_bytes, cudaStream_t st);
 cudaError_t mqa_tc_device_error(int* code);
+// q_hat operand tiles of the two kernels below (split: hi + lo parts) and the cos / sin of the
+// query positions
+size_t q_tiles_bytes(const MqaArgs& a, bool split);
+size_t q_rope_bytes(const MqaArgs& a);
+cudaError_t launch_q_tiles(const MqaArgs& a, bool split, void* tiles, void* rope, cudaStream_t st);
 // attention over 4-bit cache rows (c = 512, 64 RoPE dims, heads in groups of 64)
 bool attn_fp4_supported(const MqaArgs& a);
 size_t attn_fp4_workspace_bytes(const MqaArgs& a);

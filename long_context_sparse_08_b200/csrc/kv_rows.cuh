@@ -1,8 +1,8 @@
 // Building blocks of the kernels that stream a query's KV rows through the tensor cores in
 // chunks of 64 rows (attn_fp4.cu, attn_mass.cu): the row list of a query, the warp that
 // resolves a chunk's rows to addresses, the eight warps that bring one 64-value atom of every
-// row each into 128B-swizzled shared memory (widening 4-bit rows on the way), and the warps
-// that prepare q_hat.
+// row each into 128B-swizzled shared memory (widening 4-bit rows on the way). The query
+// operand comes as a tile that q_tiles.cu prepared.
 //
 // A 4-bit cache row (CSA_MIXED_MXFP4_BF16, c = 512, r = 64) is 368 bytes:
 //   bytes   0-223  448 e2m1 codes, element 2j in the low nibble of byte j
@@ -84,17 +84,14 @@ __device__ __forceinline__ void prefetch_l2(uint64_t addr, uint32_t bytes) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(addr + bytes - 1));
 }
 
-// The address warp: chunks [c0, c1) of the list, four at a time, so that four chunks share
-// the two dependent round trips (index list, page table). `code`: error code of a
-// wait that gave up; code + 5: a page id outside the pool (an evicted page is masked quietly).
-template <int kFmt>
-__device__ __forceinline__ void resolve_rows(const MqaArgs& a, const List& l, int bt, int b,
-                                             int c0, int c1, AddrRing& ring, int code) {
-  const int lane = threadIdx.x & 31;
-  const size_t row_bytes = kFmt == kFp4 ? kFp4RowBytes : kC * 2;
-  for (int j0 = c0; j0 < c1; j0 += kRing) {
-    int e[kRing][2];
-    int32_t pg[kRing][2];
+// The entries of kRing chunks and their pages, one row of each half chunk per lane: the two
+// dependent round trips (index list, page table) are shared by four chunks.
+struct RowBatch {
+  int e[kRing][2];
+  int32_t pg[kRing][2];
+  __device__ __forceinline__ void lookup(const MqaArgs& a, const List& l, int bt, int b, int j0,
+                                         int c1) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < kRing; ++i)
 #pragma unroll
@@ -112,6 +109,19 @@ __device__ __forceinline__ void resolve_rows(const MqaArgs& a, const List& l, in
         if (e[i][h] >= 0 && e[i][h] < a.n_cap)
           pg[i][h] = a.page_table[(size_t)b * a.max_pages + (uint32_t)e[i][h] / (uint32_t)a.page_rows];
       }
+  }
+};
+
+// The address warp: chunks [c0, c1) of the list, the first batch already looked up. `code`: error
+// code of a wait that gave up; code + 5: a page id outside the pool (an evicted page is masked
+// quietly).
+template <int kFmt>
+__device__ __forceinline__ void resolve_rows(RowBatch& rb, const MqaArgs& a, const List& l, int bt,
+                                             int b, int c0, int c1, AddrRing& ring, int code) {
+  const int lane = threadIdx.x & 31;
+  const size_t row_bytes = kFmt == kFp4 ? kFp4RowBytes : kC * 2;
+  for (int j0 = c0; j0 < c1; j0 += kRing) {
+    if (j0 > c0) rb.lookup(a, l, bt, b, j0, c1);
 #pragma unroll
     for (int i = 0; i < kRing; ++i) {
       const int j = j0 + i;
@@ -120,9 +130,9 @@ __device__ __forceinline__ void resolve_rows(const MqaArgs& a, const List& l, in
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (j < l.nc) {
-          const int32_t p = pg[i][h];
+          const int32_t p = rb.pg[i][h];
           if (p >= 0 && p < a.n_pages) {
-            const size_t row = (size_t)p * a.page_rows + (uint32_t)e[i][h] % (uint32_t)a.page_rows;
+            const size_t row = (size_t)p * a.page_rows + (uint32_t)rb.e[i][h] % (uint32_t)a.page_rows;
             src[h] = reinterpret_cast<uint64_t>(a.kv) + row * row_bytes;
           } else if (p != kEvicted) {
             set_error(code + 5);
@@ -270,55 +280,7 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// cos / sin of the query position for the 32 RoPE pairs.
-struct RopeTable {
-  float cs[kR / 2], sn[kR / 2];
-};
-
-// The 16 q_hat values of a lane (dims 8 lane .. and 256 + 8 lane ..) of one head, fp32:
-// RoPE_t(RMSNorm(q) * w). `raw`: the lane's two 16-byte pieces of the head's bf16 row.
-__device__ __forceinline__ void qhat_lane(const uint4 (&raw)[2], const float (&w)[16], float eps,
-                                          const RopeTable& rope, float (&y)[16]) {
-  const int lane = threadIdx.x & 31;
-  float ss = 0.f;
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const uint32_t w4[4] = {raw[half].x, raw[half].y, raw[half].z, raw[half].w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float lo = __uint_as_float(w4[k] << 16), hi = __uint_as_float(w4[k] & 0xffff0000u);
-      y[8 * half + 2 * k] = lo;
-      y[8 * half + 2 * k + 1] = hi;
-      ss = fmaf(lo, lo, ss);
-      ss = fmaf(hi, hi, ss);
-    }
-  }
-  const float rstd = 1.f / sqrtf(warp_sum(ss) / (float)kC + eps);
-#pragma unroll
-  for (int k = 0; k < 16; ++k) y[k] = y[k] * rstd * w[k];
-  if (lane >= 24) {  // dims 256 + 8 lane >= 448
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int p = 4 * (lane - 24) + k;
-      const float c = rope.cs[p], s = rope.sn[p], u = y[8 + 2 * k], v = y[9 + 2 * k];
-      y[8 + 2 * k] = u * c - v * s;
-      y[9 + 2 * k] = u * s + v * c;
-    }
-  }
-}
-
-__device__ __forceinline__ void qhat_weights(const void* q_rms_w, float (&w)[16]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int half = 0; half < 2; ++half)
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      w[8 * half + k] = q_rms_w ? __bfloat162float(static_cast<const __nv_bfloat16*>(
-                                      q_rms_w)[256 * half + 8 * lane + k])
-                                : 1.f;
-}
-
-// Eight fp32 values to 16-bit operands (f16 for 4-bit caches, else bf16).
+// Two fp32 values to 16-bit operands (f16 for 4-bit caches, else bf16).
 template <int kFmt>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   if constexpr (kFmt == kFp4) {
@@ -338,6 +300,16 @@ template <int kFmt>
 __device__ __forceinline__ float unpack_hi(uint32_t w) {
   if constexpr (kFmt == kFp4) return __half2float(__ushort_as_half((unsigned short)(w >> 16)));
   else return __uint_as_float(w & 0xffff0000u);
+}
+
+// `bytes` bytes (a multiple of 16) of device memory into shared memory, both 16-byte aligned.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
 }
 
 // The gather warps' loop over chunks [c0, c1): kBufs KV buffers of kAtoms atoms at `kv`, a full
