@@ -59,18 +59,16 @@ enum { kErrRing = 211, kErrGather = 212, kErrMma = 214, kErrSoftmax = 215 };
 
 struct Smem {
   AddrRing ring;
-  uint64_t kv_full[kBuf], kv_free[kBuf], s_full[kBuf], p_full[kBuf], q_full, done;
+  uint64_t kv_full[kBuf], kv_free[kBuf], s_full[kBuf], p_full[kBuf], vote[kBuf], q_full, done;
   uint32_t tmem_slot;
-  uint64_t vote[2];
   uint32_t need[4][4];  // [chunk % 4][softmax warp]: a head of the warp raised its maximum
-  float m_used[kHg], l_sum[kHg], alpha[2][kHg], fin[kHg];
-  float2 rope[kR / 2];  // cos, sin of the query's position
+  float alpha[2][kHg], fin[kHg];
 };
 
 struct Params {
   MqaArgs a;
-  int G, nsplit;
-  float* part;  // [stream][split][64 m | 64 l | 64 x 512 O], or nullptr
+  int G, nsplit, items;  // items: streams * nsplit
+  float* part;  // [stream][split][64 m | 64 l | 4 slices x 64 heads x 128 dims of O], or nullptr
   const uint8_t* tiles;  // q_hat tiles, 64 KB per stream
   const float2* rope;    // [B * T][32]
   float scale2;          // scale * log2(e)
@@ -79,6 +77,16 @@ struct Params {
 constexpr size_t kPartFloats = (size_t)kHg * (kC + 2);
 
 __device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool all_softmax(bool ok) {
+  uint32_t res;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.and.pred p, 1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(res)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return res != 0;
+}
 // A wait of one softmax warp. No barrier of the four warps follows it inside the chunk loop,
 // so a warp whose wait gives up leaves the others to their own limits.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
@@ -140,8 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
   Smem& S = *reinterpret_cast<Smem*>(base + kOffEnd);
   const MqaArgs& a = P.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int stream = blockIdx.x / P.nsplit, split = blockIdx.x % P.nsplit;
-  const int bt = stream / P.G, g = stream % P.G, b = bt / a.T, h0 = g * kHg;
+  const int step = gridDim.x;
 
   if (warp == 4) {
     if (lane == 0) {
@@ -165,22 +172,45 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
   }
   // The q_tiles launch before this one waited for everything earlier on the stream, and this
   // kernel starts after that: only the tiles themselves are waited for, below.
-  const List l = make_list(a, bt);
-  const int c0 = (int)(((int64_t)l.n_chunks * split) / P.nsplit);
-  const int c1 = (int)(((int64_t)l.n_chunks * (split + 1)) / P.nsplit);
+  Item x;
+  int64_t t_next = item_pos(a, blockIdx.x, P.G, P.nsplit);
+  x.set(a, blockIdx.x, P.G, P.nsplit, t_next);
   RowBatch rows0;
-  if (warp == 5) rows0.lookup(a, l, bt, b, c0, c1);
+  if (warp == 5) rows0.lookup(a, x, x.c0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   pdl_trigger();
   const uint32_t tmem = S.tmem_slot;
+  // Each role walks the CTA's items (one, where streams are split; several for many queries)
+  // with its own count of chunks, so the next item's rows are gathered and multiplied while the
+  // last one is finalised.
+  int w = blockIdx.x;
+  uint32_t it = 0;
+  bool ok = true;
+  auto peek = [&]() {  // the next item's position, an item ahead of its use
+    if (w + step < P.items) t_next = item_pos(a, w + step, P.G, P.nsplit);
+  };
+  auto advance = [&]() {
+    w += step;
+    if (w >= P.items) return false;
+    x.set(a, w, P.G, P.nsplit, t_next);
+    return true;
+  };
 
   if (warp >= 6) {
-    gather_loop<kFp4, kBuf, false>(base + kOffKV, c0, c1, l.nc, warp - 6, S.ring, S.kv_full,
-                                   S.kv_free, kErrGather);
+    do {
+      peek();
+      ok = gather_loop<kFp4, kBuf, false>(base + kOffKV, x, it, warp - 6, S.ring, S.kv_full,
+                                          S.kv_free, kErrGather);
+    } while (ok && advance());
   } else if (warp == 5) {
-    resolve_rows<kFp4>(rows0, a, l, bt, b, c0, c1, S.ring, kErrRing);
+    while (true) {
+      peek();
+      ok = resolve_rows<kFp4>(rows0, a, x, it, S.ring, kErrRing);
+      if (!ok || !advance()) break;
+      rows0.lookup(a, x, x.c0);
+    }
   } else if (warp == 4) {
     // ------------------------------ MMA issuer ------------------------------
     // One thread runs the whole loop: a step of it (votes, branches) costs as much as its MMAs
@@ -193,61 +223,71 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
       const uint64_t dk0 = smem_desc(sb + kOffKV, 16, 1024, kLayoutSw128);
       const uint64_t dv0 = smem_desc(sb + kOffKV, kAtomBytes, 1024, kLayoutSw128);
       const uint64_t dp0 = smem_desc(sb + kOffP, 16, 1024, kLayoutSw128);
-      // S runs at most one chunk ahead of O^T. Where both could be issued, whichever has its
-      // operands goes first, O^T before S (it frees a buffer). S tile slot i % 2 was read by the
-      // softmax of chunk i - 2 before it published P(i - 2), which this thread has waited for.
-      const int n = c1 - c0;
-      int is = 0, iv = 0;
-      bool ok = n > 0;
-      if (ok) {
-        pdl_wait();  // the tiles
-        mbar_arrive_expect_tx(&S.q_full, kAtoms * kHg * 128);
-        bulk_load(base + kOffQ, P.tiles + (size_t)stream * (kAtoms * kHg * 128), kAtoms * kHg * 128,
-                  &S.q_full);
-        ok = mbar_wait(&S.q_full, 0, kErrMma);
-      }
-      while (ok && iv < n) {
-        const int ss = is & 1, sv = iv & 1;
-        const uint32_t kp = (uint32_t)(is >> 1) & 1, pp = (uint32_t)(iv >> 1) & 1;
-        bool do_v;
-        if (iv < is && is < n && is - iv < kBuf) {
-          const long long t0 = clock64();
-          while (true) {
-            do_v = mbar_test(&S.p_full[sv], pp);
-            if (do_v || mbar_test(&S.kv_full[ss], kp)) break;
-            if (clock64() - t0 > kSpinCycles) {
-              set_error(kErrMma);
-              ok = false;
-              break;
+      constexpr uint32_t kQBytes = kAtoms * kHg * 128;
+      pdl_wait();  // the tiles
+      auto load_q = [&](int stream) {
+        mbar_arrive_expect_tx(&S.q_full, kQBytes);
+        bulk_load(base + kOffQ, P.tiles + (size_t)stream * kQBytes, kQBytes, &S.q_full);
+      };
+      load_q(x.stream);
+      uint32_t is = 0, iv = 0;  // chunks whose S and whose O^T have been issued
+      for (uint32_t item = 0; ok; ++item) {
+        peek();
+        const uint32_t first = iv, end = iv + (uint32_t)(x.c1 - x.c0);
+        ok = mbar_wait(&S.q_full, item & 1, kErrMma);
+        // S runs at most one chunk ahead of O^T. Where both could be issued, whichever has its
+        // operands goes first, O^T before S (it frees a buffer). S tile slot i % 2 was read by the
+        // softmax of chunk i - 2 before it published P(i - 2), which this thread has waited for.
+        while (ok && iv < end) {
+          const uint32_t ss = is & 1, sv = iv & 1, kp = (is >> 1) & 1, pp = (iv >> 1) & 1;
+          bool do_v;
+          if (iv < is && is < end && is - iv < kBuf) {
+            const long long t0 = clock64();
+            while (true) {
+              do_v = mbar_test(&S.p_full[sv], pp);
+              if (do_v || mbar_test(&S.kv_full[ss], kp)) break;
+              if (clock64() - t0 > kSpinCycles) {
+                set_error(kErrMma);
+                ok = false;
+                break;
+              }
             }
+          } else {
+            do_v = iv < is;
+            ok = mbar_wait(do_v ? &S.p_full[sv] : &S.kv_full[ss], do_v ? pp : kp, kErrMma);
           }
-        } else {
-          do_v = iv < is;
-          ok = mbar_wait(do_v ? &S.p_full[sv] : &S.kv_full[ss], do_v ? pp : kp, kErrMma);
+          if (!ok) break;
+          if (do_v) {
+            // P of the last chunk is there, so its S is done: q_hat may be replaced. (And P of the
+            // first chunk says that the softmax warps have read O^T of the item before.)
+            if (iv + 1 == end && w + step < P.items) load_q((int)((uint32_t)(w + step) / (uint32_t)P.nsplit));
+            tc_fence_after();
+            const uint64_t dv = dv0 + (uint64_t)(sv * (kSlotKV >> 4)),
+                           dp = dp0 + (uint64_t)(sv * (kSlotP >> 4));
+#pragma unroll
+            for (int kk = 0; kk < kRows / 16; ++kk)
+#pragma unroll
+              for (int sl = 0; sl < 4; ++sl)
+                mma_f16(tmem + kColO + 64 * sl, dv + ((sl * 2 * kAtomBytes + kk * 2048) >> 4),
+                        dp + ((kk * 32) >> 4), idO, (iv > first || kk > 0) ? 1u : 0u);
+            mma_commit(&S.kv_free[sv]);
+            ++iv;
+          } else {
+            tc_fence_after();
+            const uint64_t dk = dk0 + (uint64_t)(ss * (kSlotKV >> 4));
+#pragma unroll
+            for (int atom = 0; atom < kAtoms; ++atom)
+#pragma unroll
+              for (int kq = 0; kq < 4; ++kq)
+                mma_f16(tmem + kColS + 64 * ss, dq + ((atom * (kHg * 128) + kq * 32) >> 4),
+                        dk + ((atom * kAtomBytes + kq * 32) >> 4), idS, (atom | kq) != 0 ? 1u : 0u);
+            mma_commit(&S.s_full[ss]);
+            ++is;
+          }
         }
         if (!ok) break;
-        tc_fence_after();
-        if (do_v) {
-          const uint64_t dv = dv0 + (uint64_t)(sv * (kSlotKV >> 4)), dp = dp0 + (uint64_t)(sv * (kSlotP >> 4));
-#pragma unroll
-          for (int kk = 0; kk < kRows / 16; ++kk)
-#pragma unroll
-            for (int sl = 0; sl < 4; ++sl)
-              mma_f16(tmem + kColO + 64 * sl, dv + ((sl * 2 * kAtomBytes + kk * 2048) >> 4),
-                      dp + ((kk * 32) >> 4), idO, (iv > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(&S.kv_free[sv]);
-          ++iv;
-        } else {
-          const uint64_t dk = dk0 + (uint64_t)(ss * (kSlotKV >> 4));
-#pragma unroll
-          for (int atom = 0; atom < kAtoms; ++atom)
-#pragma unroll
-            for (int kq = 0; kq < 4; ++kq)
-              mma_f16(tmem + kColS + 64 * ss, dq + ((atom * (kHg * 128) + kq * 32) >> 4),
-                      dk + ((atom * kAtomBytes + kq * 32) >> 4), idS, (atom | kq) != 0 ? 1u : 0u);
-          mma_commit(&S.s_full[ss]);
-          ++is;
-        }
+        if (first == end && w + step < P.items) load_q((int)((uint32_t)(w + step) / (uint32_t)P.nsplit));
+        if (!advance()) break;
       }
       mma_commit(&S.done);  // fires when nothing issued here is in flight
       mbar_wait(&S.done, 0, kErrMma);
@@ -261,187 +301,205 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
     // + 1 of head 16w + t / 4 in s[4i], s[4i + 1] and of that head + 8 in s[4i + 2], s[4i + 3]:
     // neighbouring rows pair up into one f16x2 of P without an exchange.
     const int quad = lane & 3, hq = 16 * warp + (lane >> 2);
-    float mu[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
-    bool ok = true;
+    while (true) {
+      peek();
+      const uint32_t it0 = it, n = (uint32_t)(x.c1 - x.c0);
+      float mu[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
 #pragma unroll 1
-    for (int j = c0; j < c1 && ok; ++j) {
-      const int it = j - c0, slot = it % kBuf, rs = it % kRing;
-      ok = wait_warp(&S.s_full[slot], (uint32_t)(it / kBuf) & 1);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t sv[32];
-      tmem_ld_16x256b_x8(lane_base + kColS + 64 * slot, sv);
-      const uint32_t vm[2] = {S.ring.mask[rs][0], S.ring.mask[rs][1]};
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.ring.free[rs]);
-      tmem_ld_wait();
-      if ((vm[0] & vm[1]) != 0xffffffffu) {  // some row is masked
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int row = 8 * (i >> 2) + 2 * quad + (i & 1);
-          if (!((vm[row >> 5] >> (row & 31)) & 1u)) sv[i] = 0xff800000u;  // -inf
-        }
-      }
-      float cm[2], al[2], mref[2];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(sv[4 * (i >> 1) + 2 * x + (i & 1)]));
-        cm[x] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-      }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) cm[x] = fmaxf(cm[x], __shfl_xor_sync(0xffffffffu, cm[x], 1));
-#pragma unroll
-      for (int x = 0; x < 2; ++x) cm[x] = fmaxf(cm[x], __shfl_xor_sync(0xffffffffu, cm[x], 2));
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        cm[x] *= P.scale2;
-        al[x] = 1.f;
-        if (cm[x] > mu[x] + kLazy || (mu[x] == -INFINITY && cm[x] != -INFINITY)) {
-          al[x] = mu[x] == -INFINITY ? 0.f : ex2(mu[x] - cm[x]);
-          mu[x] = cm[x];
-        }
-        lsum[x] *= al[x];
-        mref[x] = mu[x] == -INFINITY ? 0.f : mu[x];
-      }
-      // the warps tell one another whether a maximum was raised, and look once P is computed
-      const bool raised = __any_sync(0xffffffffu, (al[0] != 1.f || al[1] != 1.f) && j > c0);
-      if (quad == 0) {
-        S.alpha[it & 1][hq] = al[0];
-        S.alpha[it & 1][hq + 8] = al[1];
-      }
-      if (lane == 0) S.need[it & 3][warp] = raised ? 1u : 0u;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.vote[it & 1]);
-      // p = 2^(s * scale2 - m), paired into f16x2
-      float l4[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {  // i = 2 * (column group) + head
-        const int x = i & 1;
-        const float p0 = ex2(fmaf(__uint_as_float(sv[2 * i]), P.scale2, -mref[x]));
-        const float p1 = ex2(fmaf(__uint_as_float(sv[2 * i + 1]), P.scale2, -mref[x]));
-        l4[x][0] += p0;
-        l4[x][1] += p1;
-        sv[i] = pack2<kFp4>(p0, p1);
-      }
-      lsum[0] += l4[0][0] + l4[0][1];
-      lsum[1] += l4[1][0] + l4[1][1];
-      ok = wait_warp(&S.vote[it & 1], (uint32_t)(it >> 1) & 1);
-      if (!ok) break;
-      if ((S.need[it & 3][0] | S.need[it & 3][1] | S.need[it & 3][2] | S.need[it & 3][3]) != 0) {
-        // rare: scale this warp's dims of O^T by alpha once the previous chunk's products are
-        // done (a chunk's alpha is rewritten two chunks later, after all warps published P)
-        const int pi = it - 1;
-        ok = wait_warp(&S.kv_free[pi % kBuf], (uint32_t)(pi / kBuf) & 1);
+      for (; it - it0 < n && ok; ++it) {
+        const uint32_t slot = it % kBuf, rs = it % kRing;
+        ok = wait_warp(&S.s_full[slot], (it / kBuf) & 1);
         if (!ok) break;
         tc_fence_after();
-#pragma unroll 1
-        for (int cg = 0; cg < 16; ++cg) {  // 4 slices x 4 groups of 16 heads
-          uint32_t o[16];
-          const uint32_t ta = lane_base + kColO + 16 * cg;
-          tmem_ld_x16(ta, o);
-          tmem_ld_wait();
-#pragma unroll
-          for (int h = 0; h < 16; ++h)
-            o[h] = __float_as_uint(__uint_as_float(o[h]) * S.alpha[it & 1][16 * (cg & 3) + h]);
-          tmem_st_x16(ta, o);
-        }
-        tmem_st_wait();
-      }
-      if (it >= kBuf) {  // the P buffer was read by the products of chunk j - 2
-        ok = wait_warp(&S.kv_free[slot], (uint32_t)((it - kBuf) / kBuf) & 1);
-        if (!ok) break;
-      }
-      // K-major tile [head][64 rows]: 8 x 8 pieces of 16-bit values, four a store: column groups
-      // 2 c and 2 c + 1 of heads 16w .. 16w + 7 and 16w + 8 .. 16w + 15. Lane l gives the address
-      // of row l % 8 of piece l / 8 (heads + 8 in odd pieces).
-      {
-        const uint32_t pt = smem_u32(base + kOffP + slot * kSlotP);
-        const int head = 16 * warp + (lane & 7) + ((lane >> 3) & 1) * 8;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          stmatrix_x4(pt + sw128(head, 2 * c + (lane >> 4)), sv[4 * c], sv[4 * c + 1], sv[4 * c + 2],
-                      sv[4 * c + 3]);
-      }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.p_full[slot]);
-    }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      lsum[x] += __shfl_xor_sync(0xffffffffu, lsum[x], 1);
-      lsum[x] += __shfl_xor_sync(0xffffffffu, lsum[x], 2);
-    }
-    if (quad == 0) {
-      S.m_used[hq] = mu[0];
-      S.m_used[hq + 8] = mu[1];
-      S.l_sum[hq] = lsum[0];
-      S.l_sum[hq + 8] = lsum[1];
-    }
-    // ---- epilogue ----
-    pdl_wait();  // the rotation, written beside the tiles
-    if (tid < kR / 2) S.rope[tid] = P.rope[(size_t)bt * 32 + tid];
-    if (ok && c1 > c0) {
-      const int last = c1 - c0 - 1;
-      ok = wait_warp(&S.kv_free[last % kBuf], (uint32_t)(last / kBuf) & 1);
-    }
-    bar_softmax();
-    const bool single = P.nsplit == 1;
-    float* pp = single ? nullptr : P.part + ((size_t)stream * P.nsplit + split) * kPartFloats;
-    if (tid < kHg) {
-      const float m = S.m_used[tid], lv = S.l_sum[tid];
-      if (single) {
-        const float zs = a.sink ? a.sink[h0 + tid] * 1.44269504088896341f : -INFINITY;
-        float f = 0.f;
-        if (lv != 0.f) {  // a NaN stays one
-          const float M = fmaxf(m, zs);
-          const float e = exp2f(m - M);
-          f = e / (lv * e + (zs == -INFINITY ? 0.f : exp2f(zs - M)));
-        }
-        S.fin[tid] = f;
-      } else {
-        pp[tid] = m;
-        pp[kHg + tid] = lv;
-      }
-    }
-    bar_softmax();
-    tc_fence_after();
-    const bool have = ok && c1 > c0;
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((size_t)bt * a.H + h0) * kC;
-    // O^T slice by slice: thread = dim 128 sl + tid, 64 heads
-#pragma unroll 1
-    for (int sl = 0; sl < 4; ++sl) {
-      uint32_t o[64];
-      if (have) {
-        tmem_ld_32x32b_x64(lane_base + kColO + 64 * sl, o);
+        uint32_t sv[32];
+        tmem_ld_16x256b_x8(lane_base + kColS + 64 * slot, sv);
+        const uint32_t vm[2] = {S.ring.mask[rs][0], S.ring.mask[rs][1]};
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.ring.free[rs]);
         tmem_ld_wait();
-      } else {
+        if ((vm[0] & vm[1]) != 0xffffffffu) {  // some row is masked
 #pragma unroll
-        for (int h = 0; h < 64; ++h) o[h] = 0u;
+          for (int i = 0; i < 32; ++i) {
+            const int row = 8 * (i >> 2) + 2 * quad + (i & 1);
+            if (!((vm[row >> 5] >> (row & 31)) & 1u)) sv[i] = 0xff800000u;  // -inf
+          }
+        }
+        float cm[2], al[2], mref[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(sv[4 * (i >> 1) + 2 * h + (i & 1)]));
+          cm[h] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) cm[h] = fmaxf(cm[h], __shfl_xor_sync(0xffffffffu, cm[h], 1));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) cm[h] = fmaxf(cm[h], __shfl_xor_sync(0xffffffffu, cm[h], 2));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          cm[h] *= P.scale2;
+          al[h] = 1.f;
+          if (cm[h] > mu[h] + kLazy || (mu[h] == -INFINITY && cm[h] != -INFINITY)) {
+            al[h] = mu[h] == -INFINITY ? 0.f : ex2(mu[h] - cm[h]);
+            mu[h] = cm[h];
+          }
+          lsum[h] *= al[h];
+          mref[h] = mu[h] == -INFINITY ? 0.f : mu[h];
+        }
+        // the warps tell one another whether a maximum was raised, and look once P is computed
+        const bool raised = __any_sync(0xffffffffu, (al[0] != 1.f || al[1] != 1.f) && it != it0);
+        if (quad == 0) {
+          S.alpha[it & 1][hq] = al[0];
+          S.alpha[it & 1][hq + 8] = al[1];
+        }
+        if (lane == 0) S.need[it & 3][warp] = raised ? 1u : 0u;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.vote[it & 1]);
+        // p = 2^(s * scale2 - m), paired into f16x2
+        float l4[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {  // i = 2 * (column group) + head
+          const int h = i & 1;
+          const float p0 = ex2(fmaf(__uint_as_float(sv[2 * i]), P.scale2, -mref[h]));
+          const float p1 = ex2(fmaf(__uint_as_float(sv[2 * i + 1]), P.scale2, -mref[h]));
+          l4[h][0] += p0;
+          l4[h][1] += p1;
+          sv[i] = pack2<kFp4>(p0, p1);
+        }
+        lsum[0] += l4[0][0] + l4[0][1];
+        lsum[1] += l4[1][0] + l4[1][1];
+        ok = wait_warp(&S.vote[it & 1], (it >> 1) & 1);
+        if (!ok) break;
+        if ((S.need[it & 3][0] | S.need[it & 3][1] | S.need[it & 3][2] | S.need[it & 3][3]) != 0) {
+          // rare: scale this warp's dims of O^T by alpha once the previous chunk's products are
+          // done (a chunk's alpha is rewritten two chunks later, after all warps published P)
+          ok = wait_warp(&S.kv_free[(it - 1) % kBuf], ((it - 1) / kBuf) & 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int cg = 0; cg < 16; ++cg) {  // 4 slices x 4 groups of 16 heads
+            uint32_t o[16];
+            const uint32_t ta = lane_base + kColO + 16 * cg;
+            tmem_ld_x16(ta, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int h = 0; h < 16; ++h)
+              o[h] = __float_as_uint(__uint_as_float(o[h]) * S.alpha[it & 1][16 * (cg & 3) + h]);
+            tmem_st_x16(ta, o);
+          }
+          tmem_st_wait();
+        }
+        if (it >= kBuf) {  // the P buffer was read by the products of chunk it - 2
+          ok = wait_warp(&S.kv_free[slot], ((it - kBuf) / kBuf) & 1);
+          if (!ok) break;
+        }
+        // K-major tile [head][64 rows]: 8 x 8 pieces of 16-bit values, four a store: column groups
+        // 2 c and 2 c + 1 of heads 16w .. 16w + 7 and 16w + 8 .. 16w + 15. Lane l gives the
+        // address of row l % 8 of piece l / 8 (heads + 8 in odd pieces).
+        {
+          const uint32_t pt = smem_u32(base + kOffP + slot * kSlotP);
+          const int head = 16 * warp + (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            stmatrix_x4(pt + sw128(head, 2 * c + (lane >> 4)), sv[4 * c], sv[4 * c + 1],
+                        sv[4 * c + 2], sv[4 * c + 3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.p_full[slot]);
       }
-      const int d = 128 * sl + tid;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        lsum[h] += __shfl_xor_sync(0xffffffffu, lsum[h], 1);
+        lsum[h] += __shfl_xor_sync(0xffffffffu, lsum[h], 2);
+      }
+      // ---- epilogue ----
+      pdl_wait();  // the rotation, written beside the tiles
+      const int h0 = (x.stream - x.bt * P.G) * kHg;
+      const bool single = P.nsplit == 1;
+      float* pp = P.part + ((size_t)x.stream * P.nsplit + x.split) * kPartFloats;
+      if (quad == 0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int head = hq + 8 * h;
+          if (single) {
+            const float zs = a.sink ? a.sink[h0 + head] * 1.44269504088896341f : -INFINITY;
+            float f = 0.f;
+            if (lsum[h] != 0.f) {  // a NaN stays one
+              const float M = fmaxf(mu[h], zs);
+              const float e = exp2f(mu[h] - M);
+              f = e / (lsum[h] * e + (zs == -INFINITY ? 0.f : exp2f(zs - M)));
+            }
+            S.fin[head] = f;
+          } else {
+            pp[head] = mu[h];
+            pp[kHg + head] = lsum[h];
+          }
+        }
+      }
+      if (ok && n > 0) ok = wait_warp(&S.kv_free[(it - 1) % kBuf], ((it - 1) / kBuf) & 1);
+      const bool have = ok && n > 0;
+      bar_softmax();  // S.fin
+      tc_fence_after();
       if (single) {
-        float cs = 1.f, sn = 0.f;
-        const bool rot = d >= kNope;
-        if (rot) {
-          cs = S.rope[(d - kNope) >> 1].x;
-          sn = -S.rope[(d - kNope) >> 1].y;  // rotation by -t
-        }
+        // thread = dim 128 sl + tid; the two threads of a pair of dims store one head's pair each
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((size_t)x.bt * a.H + h0) * kC;
+#pragma unroll 1
+        for (int sl = 0; sl < 4; ++sl) {
+          uint32_t o[64];
+          if (have) {
+            tmem_ld_32x32b_x64(lane_base + kColO + 64 * sl, o);
+            tmem_ld_wait();
+          } else {
 #pragma unroll
-        for (int h = 0; h < 64; ++h) {
-          const float y = __uint_as_float(o[h]) * S.fin[h];
-          const float yp = __shfl_xor_sync(0xffffffffu, y, 1);
-          float z = y;
-          if (rot) z = (d & 1) == 0 ? y * cs - yp * sn : yp * sn + y * cs;
-          out[(size_t)h * kC + d] = __float2bfloat16_rn(z);
+            for (int h = 0; h < 64; ++h) o[h] = 0u;
+          }
+          const int d = 128 * sl + tid, odd = tid & 1;
+          float2 cs = make_float2(1.f, 0.f);
+          if (d >= kNope) cs = P.rope[(size_t)x.bt * 32 + ((d - kNope) >> 1)];
+          __nv_bfloat16* at = out + (d & ~1) + (size_t)odd * kC;
+#pragma unroll
+          for (int h = 0; h < 64; h += 2) {
+            // this thread's head of the pair (h, h + 1): h for even dims, h + 1 for odd ones
+            const float y0 = __uint_as_float(o[h]) * S.fin[h];
+            const float y1 = __uint_as_float(o[h + 1]) * S.fin[h + 1];
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 1);
+            float u = odd ? got : y0, v = odd ? y1 : got;  // dims d & ~1, + 1 of that head
+            const float ur = u * cs.x + v * cs.y, vr = v * cs.x - u * cs.y;  // rotation by -t
+            *reinterpret_cast<__nv_bfloat162*>(at + (size_t)h * kC) = __floats2bfloat162_rn(ur, vr);
+          }
         }
+        tc_fence_before();
       } else {
+        // fp32 O^T [slice][head][128 dims] through the KV buffers, which nothing uses any more,
+        // and from there in bulk: 128 KB in 4-byte stores took 2.8 us
+#pragma unroll 1
+        for (int sl = 0; sl < 4; ++sl) {
+          uint32_t o[64];
+          if (have) {
+            tmem_ld_32x32b_x64(lane_base + kColO + 64 * sl, o);
+            tmem_ld_wait();
+          } else {
 #pragma unroll
-        for (int h = 0; h < 64; ++h) pp[2 * kHg + (size_t)h * kC + d] = __uint_as_float(o[h]);
+            for (int h = 0; h < 64; ++h) o[h] = 0u;
+          }
+          float* st = reinterpret_cast<float*>(base + kOffKV) + sl * (kHg * 128) + tid;
+#pragma unroll
+          for (int h = 0; h < 64; ++h) st[h * 128] = __uint_as_float(o[h]);
+          fence_proxy_async_smem();
+          bar_softmax();
+          if (tid == 32 * sl)
+            bulk_store(pp + 2 * kHg + (size_t)sl * (kHg * 128),
+                       base + kOffKV + (size_t)sl * (kHg * 128 * 4), kHg * 128 * 4);
+        }
+        if (lane == 0) bulk_store_wait();
       }
+      // the four warps leave together; S.fin has been read before the next item writes it
+      ok = all_softmax(ok);
+      if (!ok || !advance()) break;
     }
   }
   tc_fence_before();
@@ -452,65 +510,74 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
   }
 }
 
-// Merge the partials of one head (fixed split order), add the sink, rotate by -t. kBatch splits
-// are loaded before any is used.
-template <int kBatch>
+// Merge the partials of one head, add the sink, rotate by -t. Warp w takes splits w, w + 8, ..
+// over all 512 dims (a lane 16 of them), so that every load of the block is in flight at once;
+// the eight states are then merged in a fixed order.
 __global__ void __launch_bounds__(256) k_attn_fp4_combine(const __grid_constant__ Params P) {
+  __shared__ float so[8][kC], sm[8], sl[8];
   const MqaArgs& a = P.a;
-  const int stream = blockIdx.x, h = blockIdx.y;
-  const int bt = stream / P.G, g = stream % P.G;
-  const int d = 2 * threadIdx.x, ns = P.nsplit;
+  const int stream = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bt = stream / P.G, g = stream % P.G, ns = P.nsplit;
   const float* base = P.part + (size_t)stream * ns * kPartFloats;
   pdl_wait();
   pdl_trigger();
-  const float zs = a.sink ? a.sink[g * kHg + h] * 1.44269504088896341f : -INFINITY;
-  float2 cs_sn = make_float2(1.f, 0.f);  // of +t
-  float M = zs, l = 0.f, o0 = 0.f, o1 = 0.f;
-  for (int s0 = 0; s0 < ns; s0 += kBatch) {
-    float ms[kBatch], ls[kBatch];
-    float2 os[kBatch];
+  float M = -INFINITY, l = 0.f;
+  float4 o[4];
 #pragma unroll
-    for (int s = 0; s < kBatch; ++s) {
-      const float* pp = base + (size_t)min(s0 + s, ns - 1) * kPartFloats;
-      ms[s] = pp[h];
-      ls[s] = pp[kHg + h];
-      os[s] = *reinterpret_cast<const float2*>(pp + 2 * kHg + (size_t)h * kC + d);
-    }
-    if (s0 == 0 && d >= kNope) cs_sn = P.rope[(size_t)bt * 32 + ((d - kNope) >> 1)];
-    float Mn = M;
+  for (int i = 0; i < 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int s = warp; s < ns; s += 8) {
+    const float* pp = base + (size_t)s * kPartFloats;
+    const float m = pp[h], ls = pp[kHg + h];
+    float4 v[4];
 #pragma unroll
-    for (int s = 0; s < kBatch; ++s)
-      if (s0 + s < ns) Mn = fmaxf(Mn, ms[s]);
-    if (Mn == -INFINITY) continue;  // no row and no sink so far
-    const float f0 = exp2f(M - Mn);
-    l *= f0;
-    o0 *= f0;
-    o1 *= f0;
+    for (int i = 0; i < 4; ++i)
+      v[i] = *reinterpret_cast<const float4*>(pp + 2 * kHg + i * (kHg * 128) + h * 128 + 4 * lane);
+    if (m == -INFINITY) continue;  // no row
+    const float Mn = fmaxf(M, m), f0 = exp2f(M - Mn), f = exp2f(m - Mn);
     M = Mn;
+    l = l * f0 + ls * f;
 #pragma unroll
-    for (int s = 0; s < kBatch; ++s) {
-      if (s0 + s < ns && ms[s] != -INFINITY) {
-        const float f = exp2f(ms[s] - M);
-        l = fmaf(ls[s], f, l);
-        o0 = fmaf(os[s].x, f, o0);
-        o1 = fmaf(os[s].y, f, o1);
-      }
+    for (int i = 0; i < 4; ++i) {
+      o[i].x = o[i].x * f0 + v[i].x * f;
+      o[i].y = o[i].y * f0 + v[i].y * f;
+      o[i].z = o[i].z * f0 + v[i].z * f;
+      o[i].w = o[i].w * f0 + v[i].w * f;
     }
   }
-  float y0 = 0.f, y1 = 0.f;
-  if (l != 0.f) {  // a NaN stays one
-    const float den = l + (zs == -INFINITY ? 0.f : exp2f(zs - M));
-    y0 = o0 / den;
-    y1 = o1 / den;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(&so[warp][128 * i + 4 * lane]) = o[i];
+  if (lane == 0) {
+    sm[warp] = M;
+    sl[warp] = l;
   }
-  if (d >= kNope) {
-    const float u0 = y0 * cs_sn.x + y1 * cs_sn.y, u1 = y1 * cs_sn.x - y0 * cs_sn.y;
-    y0 = u0;
-    y1 = u1;
+  const int d = 2 * threadIdx.x;
+  float2 cs = make_float2(1.f, 0.f);  // of +t
+  if (d >= kNope) cs = P.rope[(size_t)bt * 32 + ((d - kNope) >> 1)];
+  const float zs = a.sink ? a.sink[g * kHg + h] * 1.44269504088896341f : -INFINITY;
+  __syncthreads();
+  M = zs;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) M = fmaxf(M, sm[i]);
+  float den = 0.f, u = 0.f, v = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (sm[i] != -INFINITY) {
+      const float f = exp2f(sm[i] - M);
+      den = fmaf(sl[i], f, den);
+      u = fmaf(so[i][d], f, u);
+      v = fmaf(so[i][d + 1], f, v);
+    }
   }
+  if (den != 0.f) {  // a NaN stays one
+    den += zs == -INFINITY ? 0.f : exp2f(zs - M);
+    u /= den;
+    v /= den;
+  }
+  const float ur = u * cs.x + v * cs.y, vr = v * cs.x - u * cs.y;
   __nv_bfloat16* out =
       static_cast<__nv_bfloat16*>(a.out) + ((size_t)bt * a.H + g * kHg + h) * kC + d;
-  *reinterpret_cast<__nv_bfloat162*>(out) = __floats2bfloat162_rn(y0, y1);
+  *reinterpret_cast<__nv_bfloat162*>(out) = __floats2bfloat162_rn(ur, vr);
 }
 
 // CTAs per stream: as many as fill the SMs, at most one per chunk of the longest list, at
@@ -556,10 +623,11 @@ cudaError_t launch_attn_fp4(const MqaArgs& a, void* ws, size_t ws_bytes, cudaStr
   if (e != cudaSuccess) return e;
   e = launch_q_tiles(a, false, w, w + q_tiles_bytes(a, false), st);
   if (e != cudaSuccess) return e;
-  e = launch(true, k_attn_fp4, dim3((unsigned)(streams * P.nsplit)), dim3(kThreads), smem, st, P);
+  P.items = (int)(streams * P.nsplit);
+  const int grid = P.items < device_sm_count() ? P.items : device_sm_count();
+  e = launch(true, k_attn_fp4, dim3((unsigned)grid), dim3(kThreads), smem, st, P);
   if (e != cudaSuccess || P.nsplit == 1) return e;
-  return launch(true, P.nsplit <= 8 ? k_attn_fp4_combine<8> : k_attn_fp4_combine<16>,
-                dim3((unsigned)streams, kHg), dim3(256), 0, st, P);
+  return launch(true, k_attn_fp4_combine, dim3((unsigned)streams, kHg), dim3(256), 0, st, P);
 }
 
 cudaError_t attn_fp4_device_error(int* code) {

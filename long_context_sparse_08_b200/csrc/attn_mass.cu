@@ -76,8 +76,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_mass_logits(const __grid_consta
   Smem& S = *reinterpret_cast<Smem*>(base + kOffEnd);
   const MqaArgs& a = P.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int stream = blockIdx.x / P.nsplit, split = blockIdx.x % P.nsplit;
-  const int bt = stream / P.G, g = stream % P.G, b = bt / a.T, h0 = g * kHg;
 
   if (warp == 4) {
     if (lane == 0) {
@@ -100,11 +98,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_mass_logits(const __grid_consta
     __syncwarp();
     tmem_alloc(&S.tmem_slot, kTmemCols);
   }
-  const List l = make_list(a, bt);
-  const int c0 = (int)(((int64_t)l.n_chunks * split) / P.nsplit);
-  const int c1 = (int)(((int64_t)l.n_chunks * (split + 1)) / P.nsplit);
+  Item x;
+  x.set(a, blockIdx.x, P.G, P.nsplit, item_pos(a, blockIdx.x, P.G, P.nsplit));
+  const int n = x.c1 - x.c0;
   RowBatch rows0;
-  if (warp == 5) rows0.lookup(a, l, bt, b, c0, c1);
+  if (warp == 5) rows0.lookup(a, x, x.c0);
   if (P.fixed != nullptr) {  // the sparse sums start at zero
     const size_t n = (size_t)a.B * a.n_cap, step = (size_t)gridDim.x * kThreads;
     for (size_t i = (size_t)blockIdx.x * kThreads + tid; i < n; i += step) P.fixed[i] = 0;
@@ -116,26 +114,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_mass_logits(const __grid_consta
   const uint32_t tmem = S.tmem_slot;
 
   if (warp >= 6) {
-    gather_loop<kFmt, 1, true>(base + kOffKV, c0, c1, l.nc, warp - 6, S.ring, S.kv_full, S.kv_free,
+    uint32_t it = 0;
+    gather_loop<kFmt, 1, true>(base + kOffKV, x, it, warp - 6, S.ring, S.kv_full, S.kv_free,
                                kErrGather);
   } else if (warp == 5) {
-    resolve_rows<kFmt>(rows0, a, l, bt, b, c0, c1, S.ring, kErrRing);
+    uint32_t it = 0;
+    resolve_rows<kFmt>(rows0, a, x, it, S.ring, kErrRing);
   } else if (warp == 4) {
     const uint32_t idS = idesc_f16(kFmt == kFp4 ? 0 : 1, kQRows, kRows);
     const uint64_t dq = smem_desc(smem_u32(base + kOffQ), 16, 1024, kLayoutSw128);
     const uint64_t dk = smem_desc(smem_u32(base + kOffKV), 16, 1024, kLayoutSw128);
-    bool ok = c0 < c1;
+    bool ok = n > 0;
     if (ok) {
       pdl_wait();  // the q_hat tiles of the launch before
       if (elect_one()) {
         mbar_arrive_expect_tx(&S.q_full, kAtoms * kQAtom);
-        bulk_load(base + kOffQ, P.tiles + (size_t)stream * (kAtoms * kQAtom), kAtoms * kQAtom, &S.q_full);
+        bulk_load(base + kOffQ, P.tiles + (size_t)x.stream * (kAtoms * kQAtom), kAtoms * kQAtom, &S.q_full);
       }
       __syncwarp();
       ok = __all_sync(0xffffffffu, mbar_wait(&S.q_full, 0, kErrMma));
     }
-    for (int j = c0; j < c1 && ok; ++j) {
-      const int it = j - c0, slot = it & 1;
+    for (int it = 0; it < n && ok; ++it) {
+      const int slot = it & 1;
       ok = __all_sync(0xffffffffu,
                       mbar_wait(&S.s_free[slot], ((uint32_t)(it >> 1) & 1) ^ 1, kErrMma));
       if (!ok) break;
@@ -165,12 +165,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_mass_logits(const __grid_consta
     //      lane i has the head's rows 0-31 of the chunk and lane i + 16 its rows 32-63 ----
     const uint32_t lane_base = tmem + ((uint32_t)(32 * warp) << 16);
     const int hi_half = lane >> 4, head = 16 * warp + (lane & 15);
-    float* zrow = P.z + ((size_t)stream * kHg + head) * P.z_rows + 32 * hi_half;
+    float* zrow = P.z + ((size_t)x.stream * kHg + head) * P.z_rows + 32 * hi_half;
     float m = -INFINITY, sum = 0.f;
     bool ok = true;
 #pragma unroll 1
-    for (int j = c0; j < c1 && ok; ++j) {
-      const int it = j - c0, slot = it & 1, rs = it % kRing;
+    for (int it = 0; it < n && ok; ++it) {
+      const int j = x.c0 + it, slot = it & 1, rs = it % kRing;
       ok = __all_sync(0xffffffffu, mbar_wait(&S.s_full[slot], (uint32_t)(it >> 1) & 1, kErrRead));
       if (!ok) break;
       tc_fence_after();
@@ -184,26 +184,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_mass_logits(const __grid_consta
         mbar_arrive(&S.ring.free[rs]);
         mbar_arrive(&S.s_free[slot]);
       }
-      float x[32], cm = -INFINITY;
+      float z[32], cm = -INFINITY;
 #pragma unroll
       for (int c = 0; c < 32; ++c) {
         const float give = __uint_as_float(hi_half ? v[c] : v[32 + c]);
         const float keep = __uint_as_float(hi_half ? v[32 + c] : v[c]);
         const float got = __shfl_xor_sync(0xffffffffu, give, 16);
-        x[c] = (live >> c) & 1u ? (keep + got) * P.scale2 : -INFINITY;
-        cm = fmaxf(cm, x[c]);
+        z[c] = (live >> c) & 1u ? (keep + got) * P.scale2 : -INFINITY;
+        cm = fmaxf(cm, z[c]);
       }
-      if (j < l.nc) {
+      if (j < x.l.nc) {
         float4* dst = reinterpret_cast<float4*>(zrow + (size_t)kRows * j);
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          dst[c] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+          dst[c] = make_float4(z[4 * c], z[4 * c + 1], z[4 * c + 2], z[4 * c + 3]);
       }
       const float mn = fmaxf(m, cm);
       if (mn != -INFINITY) {
         float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < 32; ++c) s4[c & 3] += exp2f(x[c] - mn);
+        for (int c = 0; c < 32; ++c) s4[c & 3] += exp2f(z[c] - mn);
         sum = sum * exp2f(m - mn) + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
         m = mn;
       }
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mass_logits(const __grid_consta
     float t = 0.f;
     if (M != -INFINITY) t = sum * exp2f(m - M) + os * exp2f(om - M);
     if (hi_half == 0) {
-      float* pp = P.part + ((size_t)stream * P.nsplit + split) * (2 * kHg);
+      float* pp = P.part + ((size_t)x.stream * P.nsplit + x.split) * (2 * kHg);
       pp[head] = M;
       pp[kHg + head] = t;
     }
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kRedThreads) k_mass_dense(const __grid_constan
   float sum = 0.f;
   for (int t = 0; t < P.a.T; ++t) {
     const int bt = b * P.a.T + t;
-    const int n_vis = make_list(P.a, bt).n_vis;
+    const int64_t n_vis = make_list(P.a, P.a.q_pos[bt]).n_vis;
     if ((int64_t)blockIdx.x * kRedThreads >= n_vis) continue;  // the same for the whole CTA
     __syncthreads();
     for (int h = threadIdx.x; h < P.a.H; h += kRedThreads) L[h] = denominator(P, bt, h);

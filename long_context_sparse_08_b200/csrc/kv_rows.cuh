@@ -54,19 +54,42 @@ __device__ __forceinline__ uint32_t sw128(uint32_t row, uint32_t chunk) {
 // kind starts a chunk of its own, so every row of a chunk has one storage format.
 struct List {
   int64_t t, lo;
-  int n_vis, n_sel, n_w, nc, n_chunks;
+  uint32_t n_vis, n_sel, n_w;
+  int nc, n_chunks;
 };
 
-__device__ __forceinline__ List make_list(const MqaArgs& a, int bt) {
+__device__ __forceinline__ List make_list(const MqaArgs& a, int64_t t) {
   List l;
-  l.t = a.q_pos[bt];
-  l.n_vis = l.t < 0 ? 0 : (int)(l.t / a.m < a.n_cap ? l.t / a.m : a.n_cap);
-  l.n_sel = a.k > 0 ? a.k : l.n_vis;
-  l.lo = (l.t - a.n_win + 1) > 0 ? (l.t - a.n_win + 1) : 0;
-  l.n_w = (a.n_win > 0 && l.t >= 0) ? (int)(l.t - l.lo + 1) : 0;
-  l.nc = (l.n_sel + kRows - 1) / kRows;
-  l.n_chunks = l.nc + (l.n_w + kRows - 1) / kRows;
+  l.t = t;
+  l.n_vis = 0;
+  if (t >= 0) {
+    const int64_t e = t <= 0x7fffffff ? (int64_t)((uint32_t)t / (uint32_t)a.m) : t / a.m;
+    l.n_vis = (uint32_t)(e < a.n_cap ? e : a.n_cap);
+  }
+  l.n_sel = a.k > 0 ? (uint32_t)a.k : l.n_vis;
+  l.lo = (t - a.n_win + 1) > 0 ? (t - a.n_win + 1) : 0;
+  l.n_w = (a.n_win > 0 && t >= 0) ? (uint32_t)(t - l.lo + 1) : 0u;
+  l.nc = (int)((l.n_sel + (kRows - 1)) / kRows);
+  l.n_chunks = l.nc + (int)((l.n_w + (kRows - 1)) / kRows);
   return l;
+}
+
+// A work item: the chunks [c0, c1) of split `split` of stream (query, 64 heads) `stream`.
+struct Item {
+  int stream, split, bt, b, c0, c1;
+  List l;
+  __device__ __forceinline__ void set(const MqaArgs& a, int w, int G, int nsplit, int64_t t) {
+    stream = (int)((uint32_t)w / (uint32_t)nsplit);
+    split = w - stream * nsplit;
+    bt = (int)((uint32_t)stream / (uint32_t)G);
+    b = (int)((uint32_t)bt / (uint32_t)a.T);
+    l = make_list(a, t);
+    c0 = (int)(((uint64_t)l.n_chunks * (uint32_t)split) / (uint32_t)nsplit);
+    c1 = (int)(((uint64_t)l.n_chunks * (uint32_t)(split + 1)) / (uint32_t)nsplit);
+  }
+};
+__device__ __forceinline__ int64_t item_pos(const MqaArgs& a, int w, int G, int nsplit) {
+  return a.q_pos[(uint32_t)w / ((uint32_t)nsplit * (uint32_t)G)];
 }
 
 // Resolved addresses of kRing chunks (0: masked row) and their masks of valid rows.
@@ -87,85 +110,99 @@ __device__ __forceinline__ void prefetch_l2(uint64_t addr, uint32_t bytes) {
 // The entries of kRing chunks and their pages, one row of each half chunk per lane: the two
 // dependent round trips (index list, page table) are shared by four chunks.
 struct RowBatch {
-  int e[kRing][2];
-  int32_t pg[kRing][2];
-  __device__ __forceinline__ void lookup(const MqaArgs& a, const List& l, int bt, int b, int j0,
-                                         int c1) {
+  uint32_t r[kRing][2];  // row within its page
+  int32_t pg[kRing][2];  // page; kEvicted: no row
+  __device__ __forceinline__ void lookup(const MqaArgs& a, const Item& x, int j0) {
     const int lane = threadIdx.x & 31;
+    int e[kRing][2];
 #pragma unroll
     for (int i = 0; i < kRing; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int s = (j0 + i) * kRows + 32 * h + lane;
+        const uint32_t s = (uint32_t)(j0 + i) * kRows + 32 * h + lane;
         e[i][h] = -1;
-        if (j0 + i < c1 && j0 + i < l.nc && s < l.n_sel)
-          e[i][h] = a.k > 0 ? a.idx[(size_t)bt * a.k + s] : s;
+        if (j0 + i < x.c1 && s < x.l.n_sel) e[i][h] = a.k > 0 ? a.idx[(size_t)x.bt * a.k + s] : (int)s;
       }
 #pragma unroll
     for (int i = 0; i < kRing; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         pg[i][h] = kEvicted;
-        if (e[i][h] >= 0 && e[i][h] < a.n_cap)
-          pg[i][h] = a.page_table[(size_t)b * a.max_pages + (uint32_t)e[i][h] / (uint32_t)a.page_rows];
+        if (e[i][h] >= 0 && e[i][h] < a.n_cap) {
+          const uint32_t lp = (uint32_t)e[i][h] / (uint32_t)a.page_rows;
+          r[i][h] = (uint32_t)e[i][h] - lp * (uint32_t)a.page_rows;
+          pg[i][h] = a.page_table[(size_t)x.b * a.max_pages + lp];
+        }
       }
   }
 };
 
-// The address warp: chunks [c0, c1) of the list, the first batch already looked up. `code`: error
-// code of a wait that gave up; code + 5: a page id outside the pool (an evicted page is masked
-// quietly).
+// The address warp: the chunks of item x, the first batch already looked up; `it` counts the
+// CTA's chunks. `code`: error code of a wait that gave up; code + 5: a page id outside the pool
+// (an evicted page is masked quietly).
 template <int kFmt>
-__device__ __forceinline__ void resolve_rows(RowBatch& rb, const MqaArgs& a, const List& l, int bt,
-                                             int b, int c0, int c1, AddrRing& ring, int code) {
+__device__ __forceinline__ bool resolve_rows(RowBatch& rb, const MqaArgs& a, const Item& x,
+                                             uint32_t& it, AddrRing& ring, int code) {
   const int lane = threadIdx.x & 31;
-  const size_t row_bytes = kFmt == kFp4 ? kFp4RowBytes : kC * 2;
-  for (int j0 = c0; j0 < c1; j0 += kRing) {
-    if (j0 > c0) rb.lookup(a, l, bt, b, j0, c1);
+  constexpr uint32_t kRowBytes = kFmt == kFp4 ? kFp4RowBytes : kC * 2;
+  for (int j0 = x.c0; j0 < x.c1; j0 += kRing) {
+    if (j0 > x.c0) rb.lookup(a, x, j0);
 #pragma unroll
     for (int i = 0; i < kRing; ++i) {
       const int j = j0 + i;
-      if (j >= c1) break;
+      if (j >= x.c1) break;
       uint64_t src[2] = {0, 0};
+      if (j < x.l.nc) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (j < l.nc) {
+        for (int h = 0; h < 2; ++h) {
           const int32_t p = rb.pg[i][h];
-          if (p >= 0 && p < a.n_pages) {
-            const size_t row = (size_t)p * a.page_rows + (uint32_t)rb.e[i][h] % (uint32_t)a.page_rows;
-            src[h] = reinterpret_cast<uint64_t>(a.kv) + row * row_bytes;
-          } else if (p != kEvicted) {
+          if (p >= 0 && p < a.n_pages)
+            src[h] = reinterpret_cast<uint64_t>(a.kv) +
+                     ((uint64_t)(uint32_t)p * (uint32_t)a.page_rows + rb.r[i][h]) * kRowBytes;
+          else if (p != kEvicted)
             set_error(code + 5);
-          }
-        } else {
-          const int s = (j - l.nc) * kRows + 32 * h + lane;
-          if (s < l.n_w) {
-            const int64_t pos = l.lo + s;
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t s = (uint32_t)(j - x.l.nc) * kRows + 32 * h + lane;
+          if (s < x.l.n_w) {
+            const int64_t pos = x.l.lo + s;
             // win_pos0 == nullptr: the state cache's ring (position p in row p mod l_raw)
-            const int64_t rr = a.win_pos0 != nullptr ? pos - a.win_pos0[b] : pos % a.l_raw;
+            const int64_t rr = a.win_pos0 != nullptr ? pos - a.win_pos0[x.b]
+                               : pos <= 0x7fffffff   ? (int64_t)((uint32_t)pos % (uint32_t)a.l_raw)
+                                                     : pos % a.l_raw;
             if (rr >= 0 && rr < a.l_raw)
-              src[h] = reinterpret_cast<uint64_t>(a.win) + ((size_t)b * a.l_raw + rr) * (kC * 2);
+              src[h] = reinterpret_cast<uint64_t>(a.win) + ((uint64_t)x.b * a.l_raw + rr) * (kC * 2);
           }
         }
       }
-      // towards L2 while the gather warps are still up to four chunks behind
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (src[h] != 0) prefetch_l2(src[h], j < l.nc ? (uint32_t)row_bytes : kC * 2);
-      const int it = j - c0;
-      if (!__all_sync(0xffffffffu, mbar_wait(&ring.free[it % kRing],
-                                             ((uint32_t)(it / kRing) & 1) ^ 1, code)))
-        return;
+      const uint32_t rs = it % kRing;
+      if (!__all_sync(0xffffffffu, mbar_wait(&ring.free[rs], ((it / kRing) & 1) ^ 1, code)))
+        return false;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        ring.src[it % kRing][32 * h + lane] = src[h];
+        ring.src[rs][32 * h + lane] = src[h];
         const uint32_t m = __ballot_sync(0xffffffffu, src[h] != 0);
-        if (lane == 0) ring.mask[it % kRing][h] = m;
+        if (lane == 0) ring.mask[rs][h] = m;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ring.full[it % kRing]);
+      if (lane == 0) mbar_arrive(&ring.full[rs]);
+      // towards L2 while the gather warps are still chunks behind; one instruction serves 32
+      // rows (the bulk form, one row each, took 80 cycles a row)
+      if (j > x.c0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (src[h] != 0) {
+            const uint32_t bytes = j < x.l.nc ? kRowBytes : kC * 2;
+            for (uint32_t o = 0; o < bytes; o += 128)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(src[h] + o));
+          }
+      }
+      ++it;
     }
   }
+  return true;
 }
 
 // Eight e2m1 codes (a 32-bit word, element 0 in the low nibble) times the f16x2 scale.
@@ -302,7 +339,8 @@ __device__ __forceinline__ float unpack_hi(uint32_t w) {
   else return __uint_as_float(w & 0xffff0000u);
 }
 
-// `bytes` bytes (a multiple of 16) of device memory into shared memory, both 16-byte aligned.
+// `bytes` bytes (a multiple of 16) of device memory into shared memory, both 16-byte aligned;
+// and back, in this thread's bulk group.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
                                           uint64_t* bar) {
   asm volatile(
@@ -312,33 +350,43 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// The gather warps' loop over chunks [c0, c1): kBufs KV buffers of kAtoms atoms at `kv`, a full
-// and a free barrier per buffer (full: one arrival per warp), or with kPerAtom per (buffer,
-// atom), so that an atom is multiplied and given back by itself. Loads of a chunk are
-// issued before the wait for its buffer.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                   reinterpret_cast<uint64_t>(dst)),
+               "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_store_wait() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// The gather warps' loop over the chunks of an item: kBufs KV buffers of kAtoms atoms at `kv`, a
+// full and a free barrier per buffer (full: one arrival per warp), or with kPerAtom per
+// (buffer, atom), so that an atom is multiplied and given back by itself. Loads of a chunk are
+// issued before the wait for its buffer. `it` counts the CTA's chunks.
 template <int kFmt, int kBufs, bool kPerAtom>
-__device__ __forceinline__ void gather_loop(uint8_t* kv, int c0, int c1, int nc, int atom,
+__device__ __forceinline__ bool gather_loop(uint8_t* kv, const Item& x, uint32_t& it, int atom,
                                             AddrRing& ring, uint64_t* full, uint64_t* free,
                                             int code) {
   const int lane = threadIdx.x & 31;
   Held v;
-  bool ok = true;
-  for (int j = c0; j < c1 && ok; ++j) {
-    const int it = j - c0, rs = it % kRing, slot = it % kBufs;
-    ok = __all_sync(0xffffffffu, mbar_wait(&ring.full[rs], (uint32_t)(it / kRing) & 1, code));
-    if (!ok) break;
-    const bool cache = j < nc;
+  for (int j = x.c0; j < x.c1; ++j, ++it) {
+    const uint32_t rs = it % kRing, slot = it % kBufs;
+    if (!__all_sync(0xffffffffu, mbar_wait(&ring.full[rs], (it / kRing) & 1, code))) return false;
+    const bool cache = j < x.l.nc;
     load_atom<kFmt>(v, ring.src[rs], cache, atom);
     __syncwarp();
     if (lane == 0) mbar_arrive(&ring.free[rs]);
-    ok = __all_sync(0xffffffffu, mbar_wait(&free[kPerAtom ? slot * kAtoms + atom : slot],
-                                           ((uint32_t)(it / kBufs) & 1) ^ 1, code + 1));
-    if (!ok) break;
+    if (!__all_sync(0xffffffffu, mbar_wait(&free[kPerAtom ? slot * kAtoms + atom : slot],
+                                           ((it / kBufs) & 1) ^ 1, code + 1)))
+      return false;
     store_atom<kFmt>(v, kv + (size_t)(slot * kAtoms + atom) * kAtomBytes, cache, atom);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&full[kPerAtom ? slot * kAtoms + atom : slot]);
   }
+  return true;
 }
 
 }  // namespace rows
