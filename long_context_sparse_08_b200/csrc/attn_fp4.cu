@@ -14,8 +14,8 @@
 //   S[64 heads x 64 rows] = q_hat . K^T          (M = 64; A = q_hat, B = the KV tile)
 //   P = 2^(S * scale * log2(e) - m_h) in f16     (four threads a head)
 //   O^T[4 x 128 dims x 64 heads] += V^T . P^T    (A = the same KV tile read MN-major)
-// q_hat comes as a prepared tile (q_tiles.cu). Warps: 0-3 softmax and epilogue; 4 issues the
-// MMAs; 5 resolves addresses; 6-13 each widen one 64-value atom of every row (kv_rows.cuh). Two
+// q_hat comes as a prepared tile (q_tiles.cu). Warps: 0-3 softmax and epilogue; 4 issues S and 6
+// O^T; 5 resolves addresses; 7-15 each widen one 64-value atom of every row (kv_rows.cuh). Two
 // KV buffers: S of chunk j + 1 may be issued before O^T of chunk j, so the tensor cores work
 // during the softmax, and the gather warps fill the buffer that O^T released.
 // The running max m_h is raised only when a chunk's max exceeds it by more than 2^11.5 (then
@@ -37,8 +37,9 @@ namespace {
 using namespace tc;
 using namespace rows;
 
-constexpr int kThreads = 14 * 32;
+constexpr int kThreads = (7 + kGatherWarps) * 32;
 constexpr int kBuf = 2;
+constexpr int kFree = 4;  // a buffer is given back in four pairs of atoms, one per slice of O^T
 constexpr float kLazy = 11.5f;  // rescale threshold (log2 units)
 constexpr int kMaxSplit = 32;
 
@@ -59,7 +60,7 @@ enum { kErrRing = 211, kErrGather = 212, kErrMma = 214, kErrSoftmax = 215 };
 
 struct Smem {
   AddrRing ring;
-  uint64_t kv_full[kBuf], kv_free[kBuf], s_full[kBuf], p_full[kBuf], vote[kBuf], q_full, done;
+  uint64_t kv_full[kBuf], kv_free[kBuf * kFree], s_full[kBuf], p_full[kBuf], vote[kBuf], q_full, done[2];
   uint32_t tmem_slot;
   uint32_t need[4][4];  // [chunk % 4][softmax warp]: a head of the warp raised its maximum
   float alpha[2][kHg], fin[kHg];
@@ -115,6 +116,12 @@ __device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t 
                "r"(b), "r"(c), "r"(d)
                : "memory");
 }
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                                  uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -154,17 +161,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
     if (lane == 0) {
       for (int i = 0; i < kRing; ++i) {
         mbar_init(&S.ring.full[i], 1);
-        mbar_init(&S.ring.free[i], 8 + 4);  // gather warps; softmax warps (the mask)
+        mbar_init(&S.ring.free[i], kGatherWarps + 4);  // and the softmax warps (the mask)
       }
       for (int i = 0; i < kBuf; ++i) {
-        mbar_init(&S.kv_full[i], 8);  // the gather warps
-        mbar_init(&S.kv_free[i], 1);
+        mbar_init(&S.kv_full[i], kGatherWarps);
+        for (int k = 0; k < kFree; ++k) mbar_init(&S.kv_free[i * kFree + k], 1);
         mbar_init(&S.s_full[i], 1);
         mbar_init(&S.p_full[i], 4);
         mbar_init(&S.vote[i], 4);
       }
       mbar_init(&S.q_full, 1);
-      mbar_init(&S.done, 1);
+      for (int i = 0; i < 2; ++i) mbar_init(&S.done[i], 1);
       fence_barrier_init();
     }
     __syncwarp();
@@ -198,12 +205,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
     return true;
   };
 
-  if (warp >= 6) {
-    do {
-      peek();
-      ok = gather_loop<kFp4, kBuf, false>(base + kOffKV, x, it, warp - 6, S.ring, S.kv_full,
-                                          S.kv_free, kErrGather);
-    } while (ok && advance());
+  if (warp >= 7) {
+    gather_loop<kFp4, kBuf, 1, kFree>(base + kOffKV, warp - 7, S.ring, S.kv_full, S.kv_free,
+                                      kErrGather);
   } else if (warp == 5) {
     while (true) {
       peek();
@@ -211,86 +215,80 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
       if (!ok || !advance()) break;
       rows0.lookup(a, x, x.c0);
     }
+    if (ok) resolve_end(it, S.ring, kErrRing);
   } else if (warp == 4) {
-    // ------------------------------ MMA issuer ------------------------------
-    // One thread runs the whole loop: a step of it (votes, branches) costs as much as its MMAs
-    // when the warp runs it together.
+    // ------------------------------ S ------------------------------
+    // One thread runs the whole loop (the votes and branches of a converged warp cost as much as
+    // the MMAs), and another warp issues O^T: a thread that issued both spent its time asking
+    // which of the two had its operands.
     if (elect_one()) {
-      const uint32_t idS = idesc_f16(0, kHg, kRows);             // M = 64, N = 64, both K-major
-      const uint32_t idO = idesc_f16(0, 128, kHg) | (1u << 15);  // M = 128 dims; A MN-major
+      const uint32_t idS = idesc_f16(0, kHg, kRows);  // M = 64, N = 64, both K-major
       const uint32_t sb = smem_u32(base);
       const uint64_t dq = smem_desc(sb + kOffQ, 16, 1024, kLayoutSw128);
       const uint64_t dk0 = smem_desc(sb + kOffKV, 16, 1024, kLayoutSw128);
-      const uint64_t dv0 = smem_desc(sb + kOffKV, kAtomBytes, 1024, kLayoutSw128);
-      const uint64_t dp0 = smem_desc(sb + kOffP, 16, 1024, kLayoutSw128);
       constexpr uint32_t kQBytes = kAtoms * kHg * 128;
       pdl_wait();  // the tiles
-      auto load_q = [&](int stream) {
-        mbar_arrive_expect_tx(&S.q_full, kQBytes);
-        bulk_load(base + kOffQ, P.tiles + (size_t)stream * kQBytes, kQBytes, &S.q_full);
-      };
-      load_q(x.stream);
-      uint32_t is = 0, iv = 0;  // chunks whose S and whose O^T have been issued
-      for (uint32_t item = 0; ok; ++item) {
+      for (uint32_t item = 0;; ++item) {
         peek();
-        const uint32_t first = iv, end = iv + (uint32_t)(x.c1 - x.c0);
+        mbar_arrive_expect_tx(&S.q_full, kQBytes);
+        bulk_load(base + kOffQ, P.tiles + (size_t)x.stream * kQBytes, kQBytes, &S.q_full);
         ok = mbar_wait(&S.q_full, item & 1, kErrMma);
-        // S runs at most one chunk ahead of O^T. Where both could be issued, whichever has its
-        // operands goes first, O^T before S (it frees a buffer). S tile slot i % 2 was read by the
-        // softmax of chunk i - 2 before it published P(i - 2), which this thread has waited for.
-        while (ok && iv < end) {
-          const uint32_t ss = is & 1, sv = iv & 1, kp = (is >> 1) & 1, pp = (iv >> 1) & 1;
-          bool do_v;
-          if (iv < is && is < end && is - iv < kBuf) {
-            const long long t0 = clock64();
-            while (true) {
-              do_v = mbar_test(&S.p_full[sv], pp);
-              if (do_v || mbar_test(&S.kv_full[ss], kp)) break;
-              if (clock64() - t0 > kSpinCycles) {
-                set_error(kErrMma);
-                ok = false;
-                break;
-              }
-            }
-          } else {
-            do_v = iv < is;
-            ok = mbar_wait(do_v ? &S.p_full[sv] : &S.kv_full[ss], do_v ? pp : kp, kErrMma);
-          }
+        const uint32_t end = it + (uint32_t)(x.c1 - x.c0);
+        for (; ok && it != end; ++it) {
+          const uint32_t slot = it & 1, ph = (it >> 1) & 1;
+          // the softmax of chunk it - 2 has read this S tile once it published P
+          ok = (it < 2 || mbar_wait(&S.p_full[slot], ph ^ 1, kErrMma)) &&
+               mbar_wait(&S.kv_full[slot], ph, kErrMma);
           if (!ok) break;
-          if (do_v) {
-            // P of the last chunk is there, so its S is done: q_hat may be replaced. (And P of the
-            // first chunk says that the softmax warps have read O^T of the item before.)
-            if (iv + 1 == end && w + step < P.items) load_q((int)((uint32_t)(w + step) / (uint32_t)P.nsplit));
-            tc_fence_after();
-            const uint64_t dv = dv0 + (uint64_t)(sv * (kSlotKV >> 4)),
-                           dp = dp0 + (uint64_t)(sv * (kSlotP >> 4));
+          tc_fence_after();
+          const uint64_t dk = dk0 + (uint64_t)(slot * (kSlotKV >> 4));
+#pragma unroll 1
+          for (int atom = 0; atom < kAtoms; ++atom)
+#pragma unroll
+            for (int kq = 0; kq < 4; ++kq)
+              mma_f16(tmem + kColS + 64 * slot, dq + ((atom * (kHg * 128) + kq * 32) >> 4),
+                      dk + ((atom * kAtomBytes + kq * 32) >> 4), idS, (atom | kq) != 0 ? 1u : 0u);
+          mma_commit(&S.s_full[slot]);
+        }
+        // the item's last S has read q_hat before the next one replaces it
+        if (ok && x.c1 > x.c0) ok = mbar_wait(&S.s_full[(it - 1) & 1], ((it - 1) >> 1) & 1, kErrMma);
+        if (!ok || !advance()) break;
+      }
+      mma_commit(&S.done[0]);  // fires when nothing issued here is in flight
+      mbar_wait(&S.done[0], 0, kErrMma);
+    }
+    __syncwarp();
+  } else if (warp == 6) {
+    // ------------------------------ O^T ------------------------------
+    if (elect_one()) {
+      const uint32_t idO = idesc_f16(0, 128, kHg) | (1u << 15);  // M = 128 dims; A MN-major
+      const uint32_t sb = smem_u32(base);
+      const uint64_t dv0 = smem_desc(sb + kOffKV, kAtomBytes, 1024, kLayoutSw128);
+      const uint64_t dp0 = smem_desc(sb + kOffP, 16, 1024, kLayoutSw128);
+      do {
+        peek();
+        const uint32_t first = it, end = it + (uint32_t)(x.c1 - x.c0);
+        for (; it != end; ++it) {
+          const uint32_t slot = it & 1;
+          // P says that S is done, that O^T was rescaled where needed, and, of an item's first
+          // chunk, that O^T of the item before has been read
+          ok = mbar_wait(&S.p_full[slot], (it >> 1) & 1, kErrMma);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dv = dv0 + (uint64_t)(slot * (kSlotKV >> 4)),
+                         dp = dp0 + (uint64_t)(slot * (kSlotP >> 4));
+#pragma unroll 1
+          for (int sl = 0; sl < 4; ++sl) {  // a slice's two atoms are given back by themselves
 #pragma unroll
             for (int kk = 0; kk < kRows / 16; ++kk)
-#pragma unroll
-              for (int sl = 0; sl < 4; ++sl)
-                mma_f16(tmem + kColO + 64 * sl, dv + ((sl * 2 * kAtomBytes + kk * 2048) >> 4),
-                        dp + ((kk * 32) >> 4), idO, (iv > first || kk > 0) ? 1u : 0u);
-            mma_commit(&S.kv_free[sv]);
-            ++iv;
-          } else {
-            tc_fence_after();
-            const uint64_t dk = dk0 + (uint64_t)(ss * (kSlotKV >> 4));
-#pragma unroll
-            for (int atom = 0; atom < kAtoms; ++atom)
-#pragma unroll
-              for (int kq = 0; kq < 4; ++kq)
-                mma_f16(tmem + kColS + 64 * ss, dq + ((atom * (kHg * 128) + kq * 32) >> 4),
-                        dk + ((atom * kAtomBytes + kq * 32) >> 4), idS, (atom | kq) != 0 ? 1u : 0u);
-            mma_commit(&S.s_full[ss]);
-            ++is;
+              mma_f16(tmem + kColO + 64 * sl, dv + ((sl * 2 * kAtomBytes + kk * 2048) >> 4),
+                      dp + ((kk * 32) >> 4), idO, (it != first || kk > 0) ? 1u : 0u);
+            mma_commit(&S.kv_free[slot * kFree + sl]);
           }
         }
-        if (!ok) break;
-        if (first == end && w + step < P.items) load_q((int)((uint32_t)(w + step) / (uint32_t)P.nsplit));
-        if (!advance()) break;
-      }
-      mma_commit(&S.done);  // fires when nothing issued here is in flight
-      mbar_wait(&S.done, 0, kErrMma);
+      } while (ok && advance());
+      mma_commit(&S.done[1]);
+      mbar_wait(&S.done[1], 0, kErrMma);
     }
     __syncwarp();
   } else {
@@ -301,6 +299,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
     // + 1 of head 16w + t / 4 in s[4i], s[4i + 1] and of that head + 8 in s[4i + 2], s[4i + 3]:
     // neighbouring rows pair up into one f16x2 of P without an exchange.
     const int quad = lane & 3, hq = 16 * warp + (lane >> 2);
+    // fires when every product of chunk i is done (its last slice's)
+    auto chunk_done = [&](uint32_t i) { return &S.kv_free[(i % kBuf) * kFree + kFree - 1]; };
     while (true) {
       peek();
       const uint32_t it0 = it, n = (uint32_t)(x.c1 - x.c0);
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
         if ((S.need[it & 3][0] | S.need[it & 3][1] | S.need[it & 3][2] | S.need[it & 3][3]) != 0) {
           // rare: scale this warp's dims of O^T by alpha once the previous chunk's products are
           // done (a chunk's alpha is rewritten two chunks later, after all warps published P)
-          ok = wait_warp(&S.kv_free[(it - 1) % kBuf], ((it - 1) / kBuf) & 1);
+          ok = wait_warp(chunk_done(it - 1), ((it - 1) / kBuf) & 1);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
           tmem_st_wait();
         }
         if (it >= kBuf) {  // the P buffer was read by the products of chunk it - 2
-          ok = wait_warp(&S.kv_free[slot], ((it - kBuf) / kBuf) & 1);
+          ok = wait_warp(chunk_done(it), ((it - kBuf) / kBuf) & 1);
           if (!ok) break;
         }
         // K-major tile [head][64 rows]: 8 x 8 pieces of 16-bit values, four a store: column groups
@@ -440,37 +440,75 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
           }
         }
       }
-      if (ok && n > 0) ok = wait_warp(&S.kv_free[(it - 1) % kBuf], ((it - 1) / kBuf) & 1);
+      if (ok && n > 0) ok = wait_warp(chunk_done(it - 1), ((it - 1) / kBuf) & 1);
       const bool have = ok && n > 0;
       bar_softmax();  // S.fin
       tc_fence_after();
       if (single) {
-        // thread = dim 128 sl + tid; the two threads of a pair of dims store one head's pair each
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((size_t)x.bt * a.H + h0) * kC;
+        // Per slice of 128 dims, each warp its 32 (two pieces of 16 lanes): pairs of heads become
+        // bf16x2, stored transposed into [head][128 dims] in the P buffers (idle until the next
+        // item's first P, which these warps write), then whole rows of 256 bytes go out.
+        const uint32_t st = smem_u32(base + kOffP);
+        float f0[8], f1[8];  // of heads 8 i + 2 quad, + 1
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          f0[i] = S.fin[8 * i + 2 * quad];
+          f1[i] = S.fin[8 * i + 2 * quad + 1];
+        }
+        uint8_t* out = reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(a.out) +
+                                                  ((size_t)x.bt * a.H + h0) * kC);
 #pragma unroll 1
         for (int sl = 0; sl < 4; ++sl) {
-          uint32_t o[64];
-          if (have) {
-            tmem_ld_32x32b_x64(lane_base + kColO + 64 * sl, o);
-            tmem_ld_wait();
-          } else {
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            uint32_t o[32];
 #pragma unroll
-            for (int h = 0; h < 64; ++h) o[h] = 0u;
-          }
-          const int d = 128 * sl + tid, odd = tid & 1;
-          float2 cs = make_float2(1.f, 0.f);
-          if (d >= kNope) cs = P.rope[(size_t)x.bt * 32 + ((d - kNope) >> 1)];
-          __nv_bfloat16* at = out + (d & ~1) + (size_t)odd * kC;
+            for (int i = 0; i < 32; ++i) o[i] = 0u;
+            if (have) {
+              tmem_ld_16x256b_x8(lane_base + ((uint32_t)(16 * half) << 16) + kColO + 64 * sl, o);
+              tmem_ld_wait();
+            }
+            // registers 4 i, + 1: heads 8 i + 2 quad, + 1 of dim r = lane / 4; + 2, + 3: of dim r + 8
+            float y[32];
 #pragma unroll
-          for (int h = 0; h < 64; h += 2) {
-            // this thread's head of the pair (h, h + 1): h for even dims, h + 1 for odd ones
-            const float y0 = __uint_as_float(o[h]) * S.fin[h];
-            const float y1 = __uint_as_float(o[h + 1]) * S.fin[h + 1];
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 1);
-            float u = odd ? got : y0, v = odd ? y1 : got;  // dims d & ~1, + 1 of that head
-            const float ur = u * cs.x + v * cs.y, vr = v * cs.x - u * cs.y;  // rotation by -t
-            *reinterpret_cast<__nv_bfloat162*>(at + (size_t)h * kC) = __floats2bfloat162_rn(ur, vr);
+            for (int i = 0; i < 32; ++i)
+              y[i] = __uint_as_float(o[i]) * ((i & 1) ? f1[i >> 2] : f0[i >> 2]);
+            const int d = 128 * sl + 32 * warp + 16 * half + (lane >> 2);
+            if (128 * sl + 32 * warp >= kNope) {  // rotation by -t: dims d, d ^ 1 are lanes l, l ^ 4
+              const float2 c0 = P.rope[(size_t)x.bt * 32 + ((d - kNope) >> 1)];
+              const float2 c1 = P.rope[(size_t)x.bt * 32 + ((d + 8 - kNope) >> 1)];
+              const float sg = (d & 1) ? -1.f : 1.f;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float other = __shfl_xor_sync(0xffffffffu, y[i], 4);
+                const float2 c = (i & 2) ? c1 : c0;
+                y[i] = y[i] * c.x + sg * other * c.y;
+              }
+            }
+            // pieces of 8 dims x 8 heads; the transposed store writes, for head row r of a piece,
+            // its 8 dims: piece 2 i + (dims + 8); 16-byte chunk (32 warp + 16 half) / 8 + dims + 8
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              uint32_t p[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int e = 4 * (i + (k >> 1)) + 2 * (k & 1);
+                p[k] = pack2<kBf16>(y[e], y[e + 1]);
+              }
+              const int head = 8 * (i + (lane >> 4)) + (lane & 7);
+              const int chunk = 4 * warp + 2 * half + ((lane >> 3) & 1);
+              stmatrix_x4_trans(st + head * 256 + ((chunk ^ (head & 7)) << 4), p[0], p[1], p[2], p[3]);
+            }
           }
+          bar_softmax();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int head = 16 * warp + 2 * i + (lane >> 4), chunk = lane & 15;
+            const uint4 v = *reinterpret_cast<const uint4*>(base + kOffP + head * 256 +
+                                                            ((chunk ^ (head & 7)) << 4));
+            *reinterpret_cast<uint4*>(out + (size_t)head * (kC * 2) + 256 * sl + 16 * chunk) = v;
+          }
+          bar_softmax();
         }
         tc_fence_before();
       } else {

@@ -36,7 +36,7 @@ namespace {
 using namespace tc;
 using namespace rows;
 
-constexpr int kThreads = 14 * 32;
+constexpr int kThreads = (6 + kGatherWarps) * 32;
 constexpr int kMaxSplit = 32;
 constexpr int kQRows = 128;                       // hi and lo of 64 heads
 constexpr int kOffKV = 0;
@@ -81,10 +81,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mass_logits(const __grid_consta
     if (lane == 0) {
       for (int i = 0; i < kRing; ++i) {
         mbar_init(&S.ring.full[i], 1);
-        mbar_init(&S.ring.free[i], 8 + 4);
+        mbar_init(&S.ring.free[i], kGatherWarps + 4);
       }
       for (int i = 0; i < kAtoms; ++i) {
-        mbar_init(&S.kv_full[i], 1);
+        mbar_init(&S.kv_full[i], i == kAtoms - 1 ? 2 : 1);
         mbar_init(&S.kv_free[i], 1);
       }
       for (int i = 0; i < 2; ++i) {
@@ -114,12 +114,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mass_logits(const __grid_consta
   const uint32_t tmem = S.tmem_slot;
 
   if (warp >= 6) {
-    uint32_t it = 0;
-    gather_loop<kFmt, 1, true>(base + kOffKV, x, it, warp - 6, S.ring, S.kv_full, S.kv_free,
-                               kErrGather);
+    gather_loop<kFmt, 1, kAtoms, kAtoms>(base + kOffKV, warp - 6, S.ring, S.kv_full, S.kv_free, kErrGather);
   } else if (warp == 5) {
     uint32_t it = 0;
-    resolve_rows<kFmt>(rows0, a, x, it, S.ring, kErrRing);
+    if (resolve_rows<kFmt>(rows0, a, x, it, S.ring, kErrRing)) resolve_end(it, S.ring, kErrRing);
   } else if (warp == 4) {
     const uint32_t idS = idesc_f16(kFmt == kFp4 ? 0 : 1, kQRows, kRows);
     const uint64_t dq = smem_desc(smem_u32(base + kOffQ), 16, 1024, kLayoutSw128);

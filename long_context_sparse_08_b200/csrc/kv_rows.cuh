@@ -1,6 +1,6 @@
 // Building blocks of the kernels that stream a query's KV rows through the tensor cores in
 // chunks of 64 rows (attn_fp4.cu, attn_mass.cu): the row list of a query, the warp that
-// resolves a chunk's rows to addresses, the eight warps that bring one 64-value atom of every
+// resolves a chunk's rows to addresses, the nine warps that bring one 64-value atom of every
 // row each into 128B-swizzled shared memory (widening 4-bit rows on the way). The query
 // operand comes as a tile that q_tiles.cu prepared.
 //
@@ -92,10 +92,12 @@ __device__ __forceinline__ int64_t item_pos(const MqaArgs& a, int w, int G, int 
   return a.q_pos[(uint32_t)w / ((uint32_t)nsplit * (uint32_t)G)];
 }
 
-// Resolved addresses of kRing chunks (0: masked row) and their masks of valid rows.
+// Resolved addresses of kRing chunks (0: masked row), their masks of valid rows and what they
+// hold.
+enum Kind : uint32_t { kWindow = 0, kCache = 1, kEnd = 2 };  // kEnd: no further chunk
 struct AddrRing {
   uint64_t src[kRing][kRows];
-  uint32_t mask[kRing][2];
+  uint32_t mask[kRing][2], kind[kRing];
   uint64_t full[kRing], free[kRing];
 };
 
@@ -147,18 +149,18 @@ __device__ __forceinline__ bool resolve_rows(RowBatch& rb, const MqaArgs& a, con
   constexpr uint32_t kRowBytes = kFmt == kFp4 ? kFp4RowBytes : kC * 2;
   for (int j0 = x.c0; j0 < x.c1; j0 += kRing) {
     if (j0 > x.c0) rb.lookup(a, x, j0);
-#pragma unroll
-    for (int i = 0; i < kRing; ++i) {
+    const int n = min(kRing, x.c1 - j0);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
       const int j = j0 + i;
-      if (j >= x.c1) break;
       uint64_t src[2] = {0, 0};
       if (j < x.l.nc) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int32_t p = rb.pg[i][h];
+          const int32_t p = rb.pg[0][h];
           if (p >= 0 && p < a.n_pages)
             src[h] = reinterpret_cast<uint64_t>(a.kv) +
-                     ((uint64_t)(uint32_t)p * (uint32_t)a.page_rows + rb.r[i][h]) * kRowBytes;
+                     ((uint64_t)(uint32_t)p * (uint32_t)a.page_rows + rb.r[0][h]) * kRowBytes;
           else if (p != kEvicted)
             set_error(code + 5);
         }
@@ -177,6 +179,13 @@ __device__ __forceinline__ bool resolve_rows(RowBatch& rb, const MqaArgs& a, con
           }
         }
       }
+#pragma unroll
+      for (int k = 0; k + 1 < kRing; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          rb.pg[k][h] = rb.pg[k + 1][h];
+          rb.r[k][h] = rb.r[k + 1][h];
+        }
       const uint32_t rs = it % kRing;
       if (!__all_sync(0xffffffffu, mbar_wait(&ring.free[rs], ((it / kRing) & 1) ^ 1, code)))
         return false;
@@ -186,6 +195,7 @@ __device__ __forceinline__ bool resolve_rows(RowBatch& rb, const MqaArgs& a, con
         const uint32_t m = __ballot_sync(0xffffffffu, src[h] != 0);
         if (lane == 0) ring.mask[rs][h] = m;
       }
+      if (lane == 0) ring.kind[rs] = j < x.l.nc ? kCache : kWindow;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.full[rs]);
       // towards L2 while the gather warps are still chunks behind; one instruction serves 32
@@ -203,6 +213,16 @@ __device__ __forceinline__ bool resolve_rows(RowBatch& rb, const MqaArgs& a, con
     }
   }
   return true;
+}
+
+// After the last item: tells the gather warps to stop.
+__device__ __forceinline__ void resolve_end(uint32_t it, AddrRing& ring, int code) {
+  const uint32_t rs = it % kRing;
+  if (!__all_sync(0xffffffffu, mbar_wait(&ring.free[rs], ((it / kRing) & 1) ^ 1, code))) return;
+  if ((threadIdx.x & 31) == 0) {
+    ring.kind[rs] = kEnd;
+    mbar_arrive(&ring.full[rs]);
+  }
 }
 
 // Eight e2m1 codes (a 32-bit word, element 0 in the low nibble) times the f16x2 scale.
@@ -237,85 +257,82 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// One gather warp's share of a chunk, its atom (64 values) of all 64 rows, held in registers
-// between the loads and the stores, so that the loads are in flight while the warp waits for
-// the buffer. Codes: lane -> 16-byte unit lane % 2 (one exponent block) of rows
-// lane / 2 + 16 i, four units a lane; the four 16-byte stores of eight neighbouring lanes
-// fall into distinct banks. bf16 values: unit lane % 8 of rows lane / 8 + 4 i, sixteen a lane.
-struct Held {
-  uint4 raw[16];
+// The gather warps: nine, warps 0-6 one atom (64 values) of all 64 rows each, warps 7 and 8 the
+// last atom of 32 rows each (bf16 in either format, twice the bytes of a 4-bit atom). A warp's
+// share is held in registers between the loads and the stores.
+// Codes: lane -> 16-byte unit lane % 2 (one exponent block) of rows lane / 2 + 16 i, four units
+// a lane; the four 16-byte stores of eight neighbouring lanes fall into distinct banks. bf16
+// values: unit lane % 8 of rows first + lane / 8 + 4 i, eight a lane per 32 rows.
+// The loops over a lane's units are rolled, the held values moving down through the registers:
+// sixteen warps of six kinds share the instruction caches, and with everything unrolled a
+// quarter more time went into waiting for instructions.
+constexpr int kGatherWarps = 9;
+
+struct Codes {
+  uint4 raw[4];
   uint32_t ex[4];
-};
-
-template <int kFmt>
-__device__ __forceinline__ bool holds_codes(bool cache, int atom) {
-  return kFmt == kFp4 && cache && atom < kAtoms - 1;
-}
-
-template <int kFmt>
-__device__ __forceinline__ void load_atom(Held& v, const uint64_t* src, bool cache, int atom) {
-  const int lane = threadIdx.x & 31;
-  if (holds_codes<kFmt>(cache, atom)) {
-    const int u = lane & 1;
+  __device__ __forceinline__ void load(const uint64_t* src, int atom) {
+    const int lane = threadIdx.x & 31, u = lane & 1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint8_t* p = reinterpret_cast<const uint8_t*>(src[(lane >> 1) + 16 * i]);
-      v.raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      v.ex[i] = 127;
+      raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      ex[i] = 127;
       if (p != nullptr) {
-        v.raw[i] = __ldg(reinterpret_cast<const uint4*>(p + 32 * atom + 16 * u));
-        v.ex[i] = __ldg(p + kFp4Exps + 2 * atom + u);
+        raw[i] = __ldg(reinterpret_cast<const uint4*>(p + 32 * atom + 16 * u));
+        ex[i] = __ldg(p + kFp4Exps + 2 * atom + u);
       }
     }
-  } else {
-    const int off = (kFmt == kFp4 && cache ? kFp4Rope : 128 * atom) + 16 * (lane & 7);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint8_t* p = reinterpret_cast<const uint8_t*>(src[(lane >> 3) + 4 * i]);
-      v.raw[i] = p != nullptr ? __ldg(reinterpret_cast<const uint4*>(p + off))
-                              : make_uint4(0u, 0u, 0u, 0u);
-    }
   }
-}
-
-template <int kFmt>
-__device__ __forceinline__ void store_atom(const Held& v, uint8_t* dst, bool cache, int atom) {
-  const int lane = threadIdx.x & 31;
-  if (holds_codes<kFmt>(cache, atom)) {
-    const int u = lane & 1;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = (lane >> 1) + 16 * i;
-      const __half2 s = scale_h2(v.ex[i]);
-      const uint32_t w[4] = {v.raw[i].x, v.raw[i].y, v.raw[i].z, v.raw[i].w};
+  __device__ __forceinline__ void store(uint8_t* dst) {
+    const int lane = threadIdx.x & 31, u = lane & 1;
+    uint8_t* at = dst + (lane >> 1) * 128;
+    const uint32_t r7 = (lane >> 1) & 7;
+#pragma unroll 2
+    for (int i = 0; i < 4; ++i, at += 16 * 128) {
+      const __half2 s = scale_h2(ex[0]);
+      const uint32_t w[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<uint4*>(dst + sw128(row, 4 * u + k)) = widen8(w[k], s);
-    }
-  } else {
+        *reinterpret_cast<uint4*>(at + (((4 * u + k) ^ r7) << 4)) = widen8(w[k], s);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      uint4 o = v.raw[i];
-      if constexpr (kFmt == kFp4)
-        o = make_uint4(bf16x2_to_f16x2(o.x), bf16x2_to_f16x2(o.y), bf16x2_to_f16x2(o.z),
-                       bf16x2_to_f16x2(o.w));
-      *reinterpret_cast<uint4*>(dst + sw128((lane >> 3) + 4 * i, lane & 7)) = o;
+      for (int k = 0; k < 3; ++k) {
+        raw[k] = raw[k + 1];
+        ex[k] = ex[k + 1];
+      }
     }
   }
-}
+};
 
-// Whether the phase with the given parity has completed (no waiting).
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
+template <int kFmt>
+struct Halves {  // bf16 values of rows first .. first + 31
+  uint4 raw[8];
+  __device__ __forceinline__ void load(const uint64_t* src, int offset, int first) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint8_t* p = reinterpret_cast<const uint8_t*>(src[first + (lane >> 3) + 4 * i]);
+      raw[i] = p != nullptr ? __ldg(reinterpret_cast<const uint4*>(p + offset + 16 * (lane & 7)))
+                            : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  __device__ __forceinline__ void store(uint8_t* dst, int first) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int i = 0; i < 8; i += 2) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint4 o = raw[k];
+        if constexpr (kFmt == kFp4)
+          o = make_uint4(bf16x2_to_f16x2(o.x), bf16x2_to_f16x2(o.y), bf16x2_to_f16x2(o.z),
+                         bf16x2_to_f16x2(o.w));
+        *reinterpret_cast<uint4*>(dst + sw128(first + (lane >> 3) + 4 * (i + k), lane & 7)) = o;
+      }
+#pragma unroll
+      for (int k = 0; k < 6; ++k) raw[k] = raw[k + 2];
+    }
+  }
+};
 
 // Two fp32 values to 16-bit operands (f16 for 4-bit caches, else bf16).
 template <int kFmt>
@@ -361,32 +378,95 @@ __device__ __forceinline__ void bulk_store_wait() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-// The gather warps' loop over the chunks of an item: kBufs KV buffers of kAtoms atoms at `kv`, a
-// full and a free barrier per buffer (full: one arrival per warp), or with kPerAtom per
-// (buffer, atom), so that an atom is multiplied and given back by itself. Loads of a chunk are
-// issued before the wait for its buffer. `it` counts the CTA's chunks.
-template <int kFmt, int kBufs, bool kPerAtom>
-__device__ __forceinline__ bool gather_loop(uint8_t* kv, const Item& x, uint32_t& it, int atom,
-                                            AddrRing& ring, uint64_t* full, uint64_t* free,
-                                            int code) {
+// One gather warp's loop over the CTA's chunks: kBufs KV buffers of kAtoms atoms at `kv`, kFull
+// full barriers per buffer (1: an arrival per gather warp; kAtoms: one per atom, two for the
+// last) and kFree free barriers, each for kAtoms / kFree atoms. The next chunk's loads are issued
+// once this one is stored, and are in flight until its buffer is given back.
+template <int kFmt, int kBufs, int kFull, int kFree>
+__device__ __forceinline__ void gather_loop(uint8_t* kv, int gw, AddrRing& ring, uint64_t* full,
+                                            uint64_t* free, int code) {
   const int lane = threadIdx.x & 31;
-  Held v;
-  for (int j = x.c0; j < x.c1; ++j, ++it) {
-    const uint32_t rs = it % kRing, slot = it % kBufs;
-    if (!__all_sync(0xffffffffu, mbar_wait(&ring.full[rs], (it / kRing) & 1, code))) return false;
-    const bool cache = j < x.l.nc;
-    load_atom<kFmt>(v, ring.src[rs], cache, atom);
+  const int atom = gw < kAtoms - 1 ? gw : kAtoms - 1;
+  const bool last = atom == kAtoms - 1;
+  const int first = gw == kGatherWarps - 1 ? 32 : 0;  // of a warp of the last atom
+  auto wait = [&](uint64_t* bar, uint32_t parity, int c) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, c));
+  };
+  auto address = [&](uint32_t it) {  // the chunk's kind, or kEnd
+    return wait(&ring.full[it % kRing], (it / kRing) & 1, code) ? ring.kind[it % kRing]
+                                                                : (uint32_t)kEnd;
+  };
+  auto read = [&](uint32_t it) {  // this warp has read the chunk's addresses
     __syncwarp();
-    if (lane == 0) mbar_arrive(&ring.free[rs]);
-    if (!__all_sync(0xffffffffu, mbar_wait(&free[kPerAtom ? slot * kAtoms + atom : slot],
-                                           ((it / kBufs) & 1) ^ 1, code + 1)))
-      return false;
-    store_atom<kFmt>(v, kv + (size_t)(slot * kAtoms + atom) * kAtomBytes, cache, atom);
+    if (lane == 0) mbar_arrive(&ring.free[it % kRing]);
+  };
+  auto dst_of = [&](uint32_t it) { return kv + ((it % kBufs) * kAtoms + atom) * kAtomBytes; };
+  auto buffer = [&](uint32_t it) {
+    return wait(&free[(it % kBufs) * kFree + atom / (kAtoms / kFree)], ((it / kBufs) & 1) ^ 1,
+                code + 1);
+  };
+  auto publish = [&](uint32_t it) {
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&full[kPerAtom ? slot * kAtoms + atom : slot]);
+    if (lane == 0) mbar_arrive(&full[(it % kBufs) * kFull + atom / (kAtoms / kFull)]);
+  };
+  uint32_t it = 0, kind = address(0);
+  if (kFmt == kFp4 && !last) {
+    Codes v;
+    if (kind == kCache) {
+      v.load(ring.src[0], atom);
+      read(0);
+    }
+    while (kind != kEnd) {
+      if (kind == kCache) {
+        if (!buffer(it)) return;
+        v.store(dst_of(it));
+        publish(it);
+      } else {  // window rows, in two halves
+        Halves<kFmt> h0, h1;
+        h0.load(ring.src[it % kRing], 128 * atom, 0);
+        h1.load(ring.src[it % kRing], 128 * atom, 32);
+        read(it);
+        if (!buffer(it)) return;
+        h0.store(dst_of(it), 0);
+        h1.store(dst_of(it), 32);
+        publish(it);
+      }
+      kind = address(++it);
+      if (kind == kCache) {
+        v.load(ring.src[it % kRing], atom);
+        read(it);
+      }
+    }
+  } else if (last) {
+    Halves<kFmt> v;
+    auto offset = [&](uint32_t k) { return kFmt == kFp4 && k == kCache ? kFp4Rope : 128 * atom; };
+    if (kind != kEnd) {
+      v.load(ring.src[0], offset(kind), first);
+      read(0);
+    }
+    while (kind != kEnd) {
+      if (!buffer(it)) return;
+      v.store(dst_of(it), first);
+      publish(it);
+      kind = address(++it);
+      if (kind != kEnd) {
+        v.load(ring.src[it % kRing], offset(kind), first);
+        read(it);
+      }
+    }
+  } else {  // bf16 rows: both halves, one chunk at a time
+    for (; kind != kEnd; kind = address(++it)) {
+      Halves<kFmt> h0, h1;
+      h0.load(ring.src[it % kRing], 128 * atom, 0);
+      h1.load(ring.src[it % kRing], 128 * atom, 32);
+      read(it);
+      if (!buffer(it)) return;
+      h0.store(dst_of(it), 0);
+      h1.store(dst_of(it), 32);
+      publish(it);
+    }
   }
-  return true;
 }
 
 }  // namespace rows
