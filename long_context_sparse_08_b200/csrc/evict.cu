@@ -7,11 +7,14 @@
 // last `keep_last` pages stay; the best scored others fill the budget, the lower page first
 // among equals.
 //
-//   k_evict_keys    an order-preserving 32-bit key per page (0: no page; ~0: always kept)
-//   k_evict_select  a CTA per request: the budget-th largest key by four 8-bit radix passes
-//                   over keys held in registers, then one scan places kept and evicted pages
-//   k_evict_entries the kept pages' entries as an index list
-// All of it is a few passes over 4 bytes per entry and page: the launches bound it.
+//   k_evict_keys    (pages of several entries) an order-preserving 32-bit key per page, 0 for
+//                   a page without entries, over the whole device;
+//   k_evict_select  a CTA per request: the keys in shared memory, the budget-th largest by
+//                   radix passes of 11, 11 and 10 bits (a pass that leaves nothing to decide is
+//                   the last), one scan per 8192 pages to place them, and the lists.
+// 4 bytes are read per entry and a few per page, so latencies bound it. One CTA with the keys at
+// hand beat a cluster of eight per request (18 to 40 us: seven cluster barriers and sums
+// through distributed shared memory) and a CTA that read the keys from L2 in every pass (26 us).
 #include "common.cuh"
 #include "internal.h"
 
@@ -19,187 +22,262 @@ namespace csa {
 
 namespace {
 
-constexpr int kSelThreads = 1024;
+constexpr int kThreads = 1024;
+constexpr int kPer = 8;                      // pages of a lane in a round
+constexpr int kRound = kThreads * kPer;
+constexpr int kSmemKeys = 5 * kRound;        // 160 KB; a longer table leaves its keys in L2
+constexpr int kBins = 2048;
 constexpr uint32_t kAlways = 0xffffffffu;
 
 // entries finished by the tokens up to pos, and the pages that hold them
 __device__ __forceinline__ int used_entries(const EvictArgs& a, int b) {
   const int64_t pos = a.pos[b];
-  const int64_t n = pos < 0 ? 0 : (pos + 1) / a.m;
+  if (pos < 0) return 0;
+  const int64_t n = pos < 0x7fffffff ? (int64_t)((uint32_t)(pos + 1) / (uint32_t)a.m) : (pos + 1) / a.m;
   const int64_t cap = (int64_t)a.page_rows * a.max_pages;
   return (int)(n < cap ? n : cap);
 }
-__device__ __forceinline__ int used_pages(const EvictArgs& a, int entries) {
-  return entries / a.page_rows + (entries % a.page_rows != 0 ? 1 : 0);
+__device__ __forceinline__ int pages_of(const EvictArgs& a, int entries) {
+  return (int)((uint32_t)entries / (uint32_t)a.page_rows) + ((uint32_t)entries % (uint32_t)a.page_rows != 0);
 }
 
 // order-preserving key of a weight, never 0 or ~0; a NaN is the lowest
 __device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 1u : float_key(w); }
 
-// kWarp: a warp per page (its lanes over the entries), else a thread per page
-template <bool kWarp>
-__global__ void __launch_bounds__(256) k_evict_keys(EvictArgs a, uint32_t* keys) {
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if ((kWarp ? i >> 5 : i) >= a.max_pages) return;
-  const int page = (int)(kWarp ? i >> 5 : i);
-  const int n = used_entries(a, b), used = used_pages(a, n);
-  uint32_t key = 0;
-  if (page < used && a.page_table[(size_t)b * a.max_pages + page] >= 0) {
-    if (page < a.keep_first || page >= used - a.keep_last) {
-      key = kAlways;
-    } else {
-      const float* w = a.acc + ((size_t)b * a.max_pages + page) * (size_t)a.page_rows;
-      const int rows = min(a.page_rows, n - page * a.page_rows);
-      for (int r = kWarp ? lane : 0; r < rows; r += kWarp ? 32 : 1) {
-        const uint32_t k = weight_key(w[r]);
-        key = k > key ? k : key;
-      }
-      if (kWarp) key = __reduce_max_sync(0xffffffffu, key);
-    }
-  }
-  if (!kWarp || lane == 0) keys[(size_t)b * a.max_pages + page] = key;
-}
-
-// Exclusive scan over the block of two counts packed in one word; *total: the sums.
-__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* red, uint64_t* total) {
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  uint64_t s = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t u = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += u;
-  }
-  __syncthreads();
-  if (lane == 31) red[wid] = s;
-  __syncthreads();
-  if (wid == 0) {
-    uint64_t w = red[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t u = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += u;
-    }
-    red[lane] = w;
-  }
-  __syncthreads();
-  *total = red[31];
-  return s - v + (wid > 0 ? red[wid - 1] : 0);
-}
-
-__global__ void __launch_bounds__(kSelThreads) k_evict_select(EvictArgs a, const uint32_t* keys_all) {
-  __shared__ int hist[256];
-  __shared__ uint64_t red[32];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_want;
-  const int b = blockIdx.x, tid = threadIdx.x;
-  const int n = used_entries(a, b), used = used_pages(a, n);
-  pdl_wait();
-  pdl_trigger();
-  const uint32_t* keys = keys_all + (size_t)b * a.max_pages;
-
-  // present pages
-  int mine = 0;
-  for (int k = tid; k < used; k += kSelThreads) mine += keys[k] != 0;
-  uint64_t present = 0;
-  block_scan((uint64_t)mine, red, &present);
-
-  // tau: the budget-th largest key; `want` of the pages equal to it stay
-  uint32_t tau = 0;
-  int want = 0;
-  if ((int64_t)present > a.budget) {
-    if (tid == 0) {
-      s_prefix = 0;
-      s_want = a.budget;
-    }
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      const uint32_t prefix = s_prefix, mask = shift == 24 ? 0u : ~0u << (shift + 8);
-      for (int k = tid; k < used; k += kSelThreads) {
-        const uint32_t key = keys[k];
-        if (key != 0 && (key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1);
-      }
-      __syncthreads();
-      // the digit where the count from above reaches s_want
-      if (tid < 32) {
-        int c[8], sum = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          c[i] = hist[255 - (8 * tid + i)];
-          sum += c[i];
-        }
-        int above = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int u = __shfl_up_sync(0xffffffffu, above, o);
-          if (tid >= o) above += u;
-        }
-        above -= sum;
-        const int w = s_want;
-        __syncwarp();
-        if (above < w && above + sum >= w) {
-          int run = above;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (run < w && run + c[i] >= w) {
-              s_prefix = prefix | ((uint32_t)(255 - (8 * tid + i)) << shift);
-              s_want = w - run;
-            }
-            run += c[i];
-          }
-        }
-      }
-      __syncthreads();
-    }
-    tau = s_prefix;
-    want = s_want;
-  }
-
-  // in page order: ties before a page, then kept and evicted pages
-  int ties = 0, kept = 0, gone = 0;
-  for (int k0 = 0; k0 < a.max_pages; k0 += kSelThreads) {
-    const int k = k0 + tid;
-    const size_t at = (size_t)b * a.max_pages + k;
-    const uint32_t key = k < used ? keys[k] : 0u;
-    const bool tie = key != 0 && tau != 0 && key == tau;
-    uint64_t total;
-    const int before = ties + (int)block_scan(tie ? 1 : 0, red, &total);
-    ties += (int)total;
-    const bool keep = key != 0 && (key > tau || (tie && before < want));
-    const bool out = key != 0 && !keep;
-    const uint64_t pos = block_scan((keep ? 1ull : 0ull) | (out ? 1ull << 32 : 0ull), red, &total);
-    if (k < a.max_pages) a.new_table[at] = out ? kEvicted : a.page_table[at];
-    if (keep) a.kept[(size_t)b * a.budget + kept + (int)(uint32_t)pos] = k;
-    if (out) a.evicted[(size_t)b * a.max_pages + gone + (int)(pos >> 32)] = k;
-    kept += (int)(uint32_t)total;
-    gone += (int)(total >> 32);
-  }
-  for (int i = kept + tid; i < a.budget; i += kSelThreads) a.kept[(size_t)b * a.budget + i] = -1;
-  for (int i = gone + tid; i < a.max_pages; i += kSelThreads)
-    a.evicted[(size_t)b * a.max_pages + i] = -1;
-  if (tid == 0) {
-    a.counts[3 * b] = kept;
-    a.counts[3 * b + 2] = gone;
-    // the last page may be open: it is the last kept one if it stays
-    const int open = n % a.page_rows;
-    const bool last = open != 0 && keys[used - 1] != 0 &&
-                      (keys[used - 1] > tau || (keys[used - 1] == tau && ties <= want));
-    a.counts[3 * b + 1] = kept * a.page_rows - (last ? a.page_rows - open : 0);
-  }
-}
-
-// entries of the kept pages in order; -1 behind them
-__global__ void __launch_bounds__(256) k_evict_entries(EvictArgs a) {
+// `lanes` neighbouring lanes (a power of two) per page; kVec: four entries a load
+template <bool kVec>
+__global__ void __launch_bounds__(256) k_evict_keys(EvictArgs a, uint32_t* keys, int lanes) {
   const int b = blockIdx.y;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t n_out = (int64_t)a.budget * a.page_rows;
-  const int n = used_entries(a, b);
-  pdl_wait();
-  if (i >= n_out) return;
-  const int page = a.kept[(size_t)b * a.budget + i / a.page_rows];
-  const int64_t e = page < 0 ? -1 : (int64_t)page * a.page_rows + i % a.page_rows;
-  a.entries[(size_t)b * n_out + i] = e < n ? (int32_t)e : -1;
+  const int64_t p64 = i / lanes;
+  const int n = used_entries(a, b), sub = (int)(i % lanes);
+  pdl_trigger();
+  const int page = p64 < a.max_pages ? (int)p64 : a.max_pages;  // whole warps stay for the exchange
+  uint32_t key = 0;
+  if (page < a.max_pages) {
+    const int64_t e0 = (int64_t)page * a.page_rows;
+    const int rows = (int)(n - e0 < a.page_rows ? n - e0 : a.page_rows);  // <= 0: none
+    const float* w = a.acc + (size_t)b * a.max_pages * a.page_rows + e0;
+    if (kVec) {
+      for (int r = 4 * sub; r < rows; r += 4 * lanes) {
+        const float4 v = *reinterpret_cast<const float4*>(w + r);
+        key = max(key, weight_key(v.x));
+        if (r + 1 < rows) key = max(key, weight_key(v.y));
+        if (r + 2 < rows) key = max(key, weight_key(v.z));
+        if (r + 3 < rows) key = max(key, weight_key(v.w));
+      }
+    } else {
+      for (int r = sub; r < rows; r += lanes) key = max(key, weight_key(w[r]));
+    }
+  }
+  for (int o = 1; o < lanes; o <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
+  if (sub == 0 && page < a.max_pages) keys[(size_t)b * a.max_pages + page] = key;
+}
+
+// Exclusive scan over the block; *total: the sum. The caller separates two uses of `red` by a
+// barrier (there is one inside, before the sums are read).
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* red, uint32_t* total) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  uint32_t s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += u;
+  }
+  if (lane == 31) red[wid] = s;
+  __syncthreads();
+  uint32_t w = red[lane];  // every warp scans the 32 sums for itself
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += u;
+  }
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const uint32_t before = __shfl_sync(0xffffffffu, w, (wid + 31) & 31);
+  return s - v + (wid > 0 ? before : 0);
+}
+
+// kKeys: the keys come from k_evict_keys (in `ws`), else from acc (pages of one entry). kSmem:
+// they fit shared memory, else `ws` holds them throughout.
+template <bool kKeys, bool kSmem>
+__global__ void __launch_bounds__(kThreads, 1) k_evict_select(EvictArgs a, uint32_t* ws) {
+  extern __shared__ uint32_t smem_keys[];
+  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t red[2][32];
+  __shared__ int pick[3], s_last;  // digit, keys above it, keys at it
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, pr = a.page_rows;
+  const int n = used_entries(a, b), used = pages_of(a, n);
+  uint32_t* wk = ws + (size_t)b * a.max_pages;
+  uint32_t* keys = kSmem ? smem_keys : wk;
+  const int32_t* table = a.page_table + (size_t)b * a.max_pages;
+  const float* acc = a.acc + (size_t)b * a.max_pages * pr;
+  for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
+  if (kKeys) pdl_wait();
+
+  // ---- keys: pages that are mapped, those always kept above all ----
+  int mine = 0;
+#pragma unroll 8
+  for (int k = tid; k < used; k += kThreads) {
+    uint32_t key = kKeys ? wk[k] : weight_key(acc[k]);
+    if (table[k] < 0) key = 0;
+    else if (k < a.keep_first || k >= used - a.keep_last) key = kAlways;
+    keys[k] = key;
+    mine += key != 0;
+  }
+  uint32_t total;
+  block_scan((uint32_t)mine, red[0], &total);  // (its barrier also publishes keys and bins)
+  const int present = (int)total;
+
+  // ---- which stay: those with key >> shift >= least, the budget-th largest key or its decided
+  //      high bits ----
+  uint32_t least = 0;
+  int shift = 0;
+  if (present > a.budget) {
+    int want = a.budget, top = 32;  // want: how many of the keys with the digits so far stay
+    uint32_t tau = 0;
+    bool decided = false;
+    for (int pass = 0; pass < 3 && !decided; ++pass) {
+      const int bits = pass < 2 ? 11 : 10;
+      shift = top - bits;
+#pragma unroll 4
+      for (int k = tid; k - lane < used; k += kThreads) {
+        const uint32_t key = k < used ? keys[k] : 0u;
+        const bool in = key != 0 && (pass == 0 || (key >> top) == (tau >> top));
+        if (!__any_sync(0xffffffffu, in)) continue;
+        const uint32_t digit = in ? (key >> shift) & ((1u << bits) - 1u) : kBins;
+        // equal weights: one addition for the warp (32 to one bin would go one after another)
+        if (__all_sync(0xffffffffu, digit == __shfl_sync(0xffffffffu, digit, 0))) {
+          if (lane == 0) atomicAdd(&hist[digit], 32u);
+        } else if (in) {
+          atomicAdd(&hist[digit], 1u);
+        }
+      }
+      __syncthreads();
+      // thread t: bins 2047 - 2 t and 2046 - 2 t, the highest first
+      const uint32_t c0 = hist[kBins - 1 - 2 * tid], c1 = hist[kBins - 2 - 2 * tid];
+      hist[kBins - 1 - 2 * tid] = 0;
+      hist[kBins - 2 - 2 * tid] = 0;
+      const int above = (int)block_scan(c0 + c1, red[(pass + 1) & 1], &total);
+      if (above < want && above + (int)(c0 + c1) >= want) {
+        const bool second = above + (int)c0 < want;
+        pick[0] = kBins - 1 - 2 * tid - (second ? 1 : 0);
+        pick[1] = above + (second ? (int)c0 : 0);
+        pick[2] = (int)(second ? c1 : c0);
+      }
+      __syncthreads();
+      tau |= (uint32_t)pick[0] << shift;
+      want -= pick[1];
+      top = shift;
+      decided = want == pick[2];  // all of the digit's keys stay
+    }
+    least = tau >> shift;
+    if (!decided) {
+      // more keys equal tau than stay: the first `want` in page order are raised above all
+      ++least;
+      int before = 0;
+      for (int k0 = 0, round = 0; k0 < used; k0 += kThreads, ++round) {
+        const bool tie = k0 + tid < used && keys[k0 + tid] == tau;
+        const uint32_t votes = __ballot_sync(0xffffffffu, tie);
+        uint32_t at = block_scan(lane == 0 ? (uint32_t)__popc(votes) : 0u, red[round & 1], &total);
+        at = __shfl_sync(0xffffffffu, at, 0) + __popc(votes & ((1u << lane) - 1u));
+        if (tie && before + (int)at < want) keys[k0 + tid] = kAlways;
+        before += (int)total;
+      }
+      __syncthreads();
+    }
+  }
+
+  // ---- placement in page order: a warp has up to 256 consecutive pages of a round, 32 at a
+  //      time; ballots count the kept and the present pages before each ----
+  const int64_t n_out = (int64_t)a.budget * pr;
+  int32_t* out_entries = a.entries != nullptr ? a.entries + (size_t)b * n_out : nullptr;
+  int32_t* out_kept = a.kept + (size_t)b * a.budget;
+  int32_t* out_gone = a.evicted + (size_t)b * a.max_pages;
+  int32_t* nt = a.new_table + (size_t)b * a.max_pages;
+  const uint32_t below = (1u << lane) - 1u;
+  int n_kept = 0, seen = 0;
+  bool last_stays = false;
+  for (int k0 = 0, round = 0; k0 < used; k0 += kRound, ++round) {
+    const int steps = min(kPer, (used - k0 + kThreads - 1) / kThreads);
+    const int first = k0 + (tid >> 5) * (32 * steps) + lane;
+    uint32_t b_keep[kPer], b_here[kPer];
+    int32_t old[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      old[i] = i < steps && first + 32 * i < used ? table[first + 32 * i] : 0;
+    uint32_t mine2 = 0;  // kept and present pages of the warp, 16 bits each
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const uint32_t key = i < steps && first + 32 * i < used ? keys[first + 32 * i] : 0u;
+      b_here[i] = __ballot_sync(0xffffffffu, key != 0);
+      b_keep[i] = __ballot_sync(0xffffffffu, key != 0 && (key >> shift) >= least);
+      mine2 += (uint32_t)__popc(b_keep[i]) + ((uint32_t)__popc(b_here[i]) << 16);
+    }
+    uint32_t all2;  // lane 0 speaks for its warp
+    uint32_t pos = block_scan(lane == 0 ? mine2 : 0u, red[round & 1], &all2);
+    pos = __shfl_sync(0xffffffffu, pos, 0);
+    int kept0 = n_kept + (int)(pos & 0xffff), here0 = seen + (int)(pos >> 16);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int page = first + 32 * i;
+      if (i >= steps || page - lane >= used) break;
+      const bool here = (b_here[i] >> lane) & 1u, keep = (b_keep[i] >> lane) & 1u;
+      const int kept = kept0 + __popc(b_keep[i] & below);
+      if (page < used) nt[page] = here && !keep ? kEvicted : old[i];
+      if (keep) {
+        out_kept[kept] = page;
+        if (kSmem) keys[kept] = (uint32_t)page;  // every key up to here has been read
+      } else if (here) {
+        out_gone[here0 + __popc(b_here[i] & below) - kept] = page;
+      }
+      if (page == used - 1) last_stays = keep;
+      kept0 += __popc(b_keep[i]);
+      here0 += __popc(b_here[i]);
+    }
+    n_kept += (int)(all2 & 0xffff);
+    seen += (int)(all2 >> 16);
+  }
+  const int n_gone = present - n_kept;
+  for (int k = used + tid; k < a.max_pages; k += kThreads)
+    a.new_table[(size_t)b * a.max_pages + k] = table[k];
+  for (int i = n_kept + tid; i < a.budget; i += kThreads) out_kept[i] = -1;
+  for (int i = n_gone + tid; i < a.max_pages; i += kThreads) out_gone[i] = -1;
+  if (tid == 0) {
+    a.counts[3 * b] = n_kept;
+    a.counts[3 * b + 2] = n_gone;
+  }
+  // whoever had the last used page knows whether it, perhaps open, stays
+  const int open = n % pr;
+  if (last_stays) a.counts[3 * b + 1] = n_kept * pr - (open != 0 ? pr - open : 0);
+  if (tid == 0) s_last = 0;
+  __syncthreads();
+  if (last_stays) s_last = 1;
+  __syncthreads();
+  if (tid == 0 && !s_last) a.counts[3 * b + 1] = n_kept * pr;
+  if (out_entries != nullptr) {
+    __syncthreads();  // the kept pages, written by this CTA
+    const bool pow2 = (pr & (pr - 1)) == 0;
+    const int log2 = 31 - __clz(pr);
+    auto page_at = [&](uint32_t q) { return (int)q < n_kept ? (kSmem ? (int)keys[q] : out_kept[q]) : -1; };
+    auto div = [&](uint32_t i) { return pow2 ? i >> log2 : i / (uint32_t)pr; };
+    if (pr % 4 == 0) {  // four entries of a page a thread (the list is then 16-byte aligned)
+#pragma unroll 4
+      for (uint32_t i = 4 * tid; i < (uint32_t)n_out; i += 4 * kThreads) {
+        const uint32_t q = div(i);
+        const int page = page_at(q), e = page * pr + (int)(i - q * (uint32_t)pr);
+        *reinterpret_cast<int4*>(out_entries + i) =
+            make_int4(page >= 0 && e < n ? e : -1, page >= 0 && e + 1 < n ? e + 1 : -1,
+                      page >= 0 && e + 2 < n ? e + 2 : -1, page >= 0 && e + 3 < n ? e + 3 : -1);
+      }
+    } else {
+#pragma unroll 4
+      for (uint32_t i = tid; i < (uint32_t)n_out; i += kThreads) {
+        const uint32_t q = div(i);
+        const int page = page_at(q), e = page * pr + (int)(i - q * (uint32_t)pr);
+        out_entries[i] = page >= 0 && e < n ? e : -1;
+      }
+    }
+  }
 }
 
 }  // namespace
@@ -210,18 +288,26 @@ size_t evict_workspace_bytes(int B, int max_pages) {
 
 cudaError_t launch_evict(const EvictArgs& a, void* ws, cudaStream_t st) {
   uint32_t* keys = static_cast<uint32_t*>(ws);
-  const bool warp = a.page_rows >= 32;
-  const int64_t threads = (int64_t)a.max_pages * (warp ? 32 : 1);
-  const dim3 grid((unsigned)((threads + 255) / 256), (unsigned)a.B);
-  cudaError_t e = warp ? launch(false, k_evict_keys<true>, grid, dim3(256), 0, st, a, keys)
-                       : launch(false, k_evict_keys<false>, grid, dim3(256), 0, st, a, keys);
+  const bool own = a.page_rows > 1, fits = a.max_pages <= kSmemKeys;
+  cudaError_t e;
+  if (own) {
+    const bool vec = a.page_rows % 4 == 0;
+    const int units = vec ? a.page_rows / 4 : a.page_rows;
+    int lanes = 1;
+    while (lanes < 32 && 2 * lanes <= units) lanes *= 2;
+    const int64_t threads = (int64_t)a.max_pages * lanes;
+    const dim3 grid((unsigned)((threads + 255) / 256), (unsigned)a.B);
+    e = launch(false, vec ? k_evict_keys<true> : k_evict_keys<false>, grid, dim3(256), 0, st, a, keys,
+               lanes);
+    if (e != cudaSuccess) return e;
+  }
+  auto kern = own ? (fits ? k_evict_select<true, true> : k_evict_select<true, false>)
+                  : (fits ? k_evict_select<false, true> : k_evict_select<false, false>);
+  const size_t smem = fits ? (size_t)a.max_pages * sizeof(uint32_t) : 0;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSmemKeys * (int)sizeof(uint32_t));
   if (e != cudaSuccess) return e;
-  e = launch(true, k_evict_select, dim3((unsigned)a.B), dim3(kSelThreads), 0, st, a,
-             (const uint32_t*)keys);
-  if (e != cudaSuccess || a.entries == nullptr) return e;
-  const int64_t n_out = (int64_t)a.budget * a.page_rows;
-  return launch(true, k_evict_entries, dim3((unsigned)((n_out + 255) / 256), (unsigned)a.B),
-                dim3(256), 0, st, a);
+  return launch(own, kern, dim3((unsigned)a.B), dim3(kThreads), smem, st, a, keys);
 }
 
 }  // namespace csa

@@ -132,7 +132,7 @@ def plain_evict(m, page_rows, pos, acc, table, budget, first, last):
         n = min(max(pos[b] + 1, 0) // m, P * page_rows)
         used = -(-n // page_rows)
         live = [k for k in range(used) if table[b, k] >= 0]
-        always = [k for k in live if k < first or k >= used - last]
+        always = {k for k in live if k < first or k >= used - last}
 
         def score(k):
             w = acc[b, k * page_rows:min((k + 1) * page_rows, n)].astype(np.float64)
@@ -144,8 +144,9 @@ def plain_evict(m, page_rows, pos, acc, table, budget, first, last):
             return (nan, -score(k), k)
 
         rest = sorted((k for k in live if k not in always), key=rank)
-        keep = sorted(always + rest[:max(0, budget - len(always))])
-        gone = [k for k in live if k not in keep]
+        keep = sorted(list(always) + rest[:max(0, budget - len(always))])
+        stay = set(keep)
+        gone = [k for k in live if k not in stay]
         ent = [e for k in keep for e in range(k * page_rows, min((k + 1) * page_rows, n))]
         out["table"][b, gone] = -2
         out["kept"][b, :len(keep)] = keep
@@ -175,7 +176,7 @@ def run_evict(m, page_rows, pos, acc, table, budget, first, last, in_place=False
 @pytest.mark.parametrize("pages,page_rows,budget,first,last,m", [
     (1, 1, 1, 0, 0, 4), (5, 3, 2, 1, 1, 4), (37, 32, 11, 2, 3, 4), (600, 1, 512, 4, 16, 128),
     (1500, 2, 700, 0, 1, 8), (5000, 5, 1, 0, 0, 4), (9000, 1, 4096, 0, 0, 128), (70, 33, 70, 3, 3, 4),
-    (2049, 64, 1024, 10, 10, 4)])
+    (2049, 64, 1024, 10, 10, 4), (20001, 4, 9000, 1, 1, 4), (3, 12, 2, 1, 0, 4)])
 @pytest.mark.parametrize("kind", ["spread", "ties", "odd"])
 def test_evict(pages, page_rows, budget, first, last, m, kind):
     g = np.random.default_rng(pages + page_rows)
@@ -202,6 +203,23 @@ def test_evict(pages, page_rows, budget, first, last, m, kind):
             assert (got[k] == want[k]).all(), (k, in_place)
     assert set(run_evict(m, page_rows, pos, acc, table, budget, first, last, entries=False)) == \
         {"table", "kept", "evicted", "counts"}
+
+
+def test_evict_more_pages_than_shared_memory_holds():
+    """Keys in the workspace (more than 40960 pages a request), and several digits to decide."""
+    g = np.random.default_rng(5)
+    pages, B = 90003, 2
+    acc = g.integers(0, 1 << 24, size=(B, pages)).astype(np.float32)
+    table = np.arange(B * pages, dtype=np.int32).reshape(B, pages)
+    table[1, ::7] = -2
+    pos = [pages - 1, pages - 5]
+    for budget, rows in ((1, 1), (50000, 1), (90000, 1), (30000, 3)):
+        w = np.repeat(acc, rows, 1)
+        p = [rows * x for x in pos]
+        want = plain_evict(1, rows, p, w, table, budget, 0, 1)
+        got = run_evict(1, rows, p, w, table, budget, 0, 1)
+        for k in want:
+            assert (got[k] == want[k]).all(), (k, budget)
 
 
 # ------------------------------- together -------------------------------

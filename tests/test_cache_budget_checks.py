@@ -137,6 +137,7 @@ def test_page_eviction():
     assert call(entries=FAKE + 4) == INVALID
     assert call(n=need - 1) == WORKSPACE
     assert call(ws=None) == WORKSPACE
+    assert call(ws=FAKE + 8) == WORKSPACE
     assert csa.evict_pages_workspace_size(1, 0) == 0
 
 
