@@ -11,16 +11,17 @@
 // cost one read of the KV tile:
 //   [hi; lo][128 x 512] . K^T[512 x 64 rows] -> TMEM, z = (hi + lo) * scale * log2(e)
 // Head 16 w + i has hi in row 32 w + i and lo in row 32 w + 16 + i, so that both lie in the
-// TMEM lanes of one warp and one exchange adds them.
+// TMEM lanes of one warp, and two loads of 16 lanes bring a thread hi and lo of the same logit.
 //   q_tiles.cu      prepares the [hi; lo] tiles;
 //   k_mass_logits   (a CTA per (query, 64 heads, split)) writes z as fp32 and, per split and
 //                   head, the running maximum and sum;
-//   k_mass_dense    adds 2^(z - L) over queries and heads for one entry per thread;
-//   k_mass_sparse   does so for one list slot per thread and adds the result to a 64-bit
-//                   fixed-point array (2^-40), whose order of additions changes nothing;
+//   k_mass_dense    adds 2^(z - L) over queries and heads, four threads to an entry;
+//   k_mass_sparse   does so for a list slot and adds the result to a 64-bit fixed-point array
+//                   (2^-40), whose order of additions changes nothing;
 //   k_mass_finish   acc = decay * acc + that array.
-// The KV tile is single-buffered, but each 64-value atom is given back as soon as its
-// products are done, so the gather warps refill atom 0 while atoms 1-7 are multiplied.
+// The KV tile is single-buffered, but each pair of 64-value atoms is given back as soon as its
+// products are done, so the gather warps refill the first while the others are multiplied. A
+// chunk's logits leave as one bulk copy of 16 KB from a staged tile.
 #include <cmath>
 
 #include "common.cuh"
@@ -42,7 +43,10 @@ constexpr int kQRows = 128;                       // hi and lo of 64 heads
 constexpr int kOffKV = 0;
 constexpr int kOffQ = kAtoms * kAtomBytes;        // [atom][row][128 B]
 constexpr int kQAtom = kQRows * 128;
-constexpr int kOffEnd = kOffQ + kAtoms * kQAtom;
+constexpr int kOffZ = kOffQ + kAtoms * kQAtom;    // one staged tile of logits
+constexpr int kTile = kHg * kRows;
+constexpr int kOffEnd = kOffZ + kTile * 4;
+constexpr int kPairs = kAtoms / 2;                // pairs of atoms, given back one by one
 constexpr uint32_t kTmemCols = 128;               // two S tiles of 64 columns
 constexpr float kFixed = 1099511627776.f;         // 2^40
 constexpr unsigned long long kNotFinite = 1ull << 63;
@@ -53,21 +57,33 @@ enum { kErrRing = 221, kErrGather = 222, kErrMma = 224, kErrRead = 225 };
 
 struct Smem {
   AddrRing ring;
-  uint64_t kv_full[kAtoms], kv_free[kAtoms], s_full[2], s_free[2], q_full, done;
+  uint64_t kv_full[kPairs], kv_free[kPairs], s_full[2], s_free[2], q_full, done;
   uint32_t tmem_slot;
 };
 
 struct Params {
   MqaArgs a;
   int G, nsplit;
-  int64_t z_rows;            // rows of a head's z (a multiple of 64)
-  float* z;                  // [stream][64][z_rows]
+  int64_t z_tiles;           // chunks of a stream's z
+  float* z;                  // [stream][chunk][64 heads][64 rows], segments permuted
   float* part;               // [stream][split][m 64 | l 64]
   unsigned long long* fixed; // [B][n_cap] (sparse)
   float* acc;
   const uint8_t* tiles;      // q_hat tiles, 128 KB per stream
   float scale2, decay;
 };
+
+__device__ __forceinline__ void bar_readers() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool all_ok(bool ok) {
+  uint32_t res;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.and.pred p, 1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(res)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return res != 0;
+}
 
 template <int kFmt>
 __global__ void __launch_bounds__(kThreads, 1) k_mass_logits(const __grid_constant__ Params P) {
@@ -83,8 +99,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_mass_logits(const __grid_consta
         mbar_init(&S.ring.full[i], 1);
         mbar_init(&S.ring.free[i], kGatherWarps + 4);
       }
-      for (int i = 0; i < kAtoms; ++i) {
-        mbar_init(&S.kv_full[i], i == kAtoms - 1 ? 2 : 1);
+      for (int i = 0; i < kPairs; ++i) {
+        mbar_init(&S.kv_full[i], i == kPairs - 1 ? 3 : 2);
         mbar_init(&S.kv_free[i], 1);
       }
       for (int i = 0; i < 2; ++i) {
@@ -114,108 +130,123 @@ __global__ void __launch_bounds__(kThreads, 1) k_mass_logits(const __grid_consta
   const uint32_t tmem = S.tmem_slot;
 
   if (warp >= 6) {
-    gather_loop<kFmt, 1, kAtoms, kAtoms>(base + kOffKV, warp - 6, S.ring, S.kv_full, S.kv_free, kErrGather);
+    gather_loop<kFmt, 1, kPairs, kPairs>(base + kOffKV, warp - 6, S.ring, S.kv_full, S.kv_free,
+                                         kErrGather);
   } else if (warp == 5) {
     uint32_t it = 0;
     if (resolve_rows<kFmt>(rows0, a, x, it, S.ring, kErrRing)) resolve_end(it, S.ring, kErrRing);
   } else if (warp == 4) {
-    const uint32_t idS = idesc_f16(kFmt == kFp4 ? 0 : 1, kQRows, kRows);
-    const uint64_t dq = smem_desc(smem_u32(base + kOffQ), 16, 1024, kLayoutSw128);
-    const uint64_t dk = smem_desc(smem_u32(base + kOffKV), 16, 1024, kLayoutSw128);
-    bool ok = n > 0;
-    if (ok) {
+    if (n > 0 && elect_one()) {  // one thread issues everything (see attn_fp4.cu)
+      const uint32_t idS = idesc_f16(kFmt == kFp4 ? 0 : 1, kQRows, kRows);
+      const uint64_t dq = smem_desc(smem_u32(base + kOffQ), 16, 1024, kLayoutSw128);
+      const uint64_t dk = smem_desc(smem_u32(base + kOffKV), 16, 1024, kLayoutSw128);
       pdl_wait();  // the q_hat tiles of the launch before
-      if (elect_one()) {
-        mbar_arrive_expect_tx(&S.q_full, kAtoms * kQAtom);
-        bulk_load(base + kOffQ, P.tiles + (size_t)x.stream * (kAtoms * kQAtom), kAtoms * kQAtom, &S.q_full);
-      }
-      __syncwarp();
-      ok = __all_sync(0xffffffffu, mbar_wait(&S.q_full, 0, kErrMma));
-    }
-    for (int it = 0; it < n && ok; ++it) {
-      const int slot = it & 1;
-      ok = __all_sync(0xffffffffu,
-                      mbar_wait(&S.s_free[slot], ((uint32_t)(it >> 1) & 1) ^ 1, kErrMma));
-      if (!ok) break;
+      mbar_arrive_expect_tx(&S.q_full, kAtoms * kQAtom);
+      bulk_load(base + kOffQ, P.tiles + (size_t)x.stream * (kAtoms * kQAtom), kAtoms * kQAtom, &S.q_full);
+      bool ok = mbar_wait(&S.q_full, 0, kErrMma);
+      for (int it = 0; it < n && ok; ++it) {
+        const int slot = it & 1;
+        ok = mbar_wait(&S.s_free[slot], ((uint32_t)(it >> 1) & 1) ^ 1, kErrMma);
+#pragma unroll 1
+        for (int p = 0; p < kPairs && ok; ++p) {
+          ok = mbar_wait(&S.kv_full[p], (uint32_t)it & 1, kErrMma);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-      for (int atom = 0; atom < kAtoms; ++atom) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&S.kv_full[atom], (uint32_t)it & 1, kErrMma));
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int kq = 0; kq < 4; ++kq)
-            mma_f16(tmem + 64 * slot, dq + ((atom * kQAtom + kq * 32) >> 4),
-                    dk + ((atom * kAtomBytes + kq * 32) >> 4), idS, (atom | kq) != 0 ? 1u : 0u);
-          mma_commit(&S.kv_free[atom]);
+          for (int kq = 0; kq < 8; ++kq) {  // two atoms of four steps
+            const int atom = kq >> 2;
+            mma_f16(tmem + 64 * slot, dq + (((2 * p + atom) * kQAtom + (kq & 3) * 32) >> 4),
+                    dk + (((2 * p + atom) * kAtomBytes + (kq & 3) * 32) >> 4), idS,
+                    (p | kq) != 0 ? 1u : 0u);
+          }
+          mma_commit(&S.kv_free[p]);
         }
+        if (ok) mma_commit(&S.s_full[slot]);
       }
-      if (!ok) break;
-      if (elect_one()) mma_commit(&S.s_full[slot]);
-      __syncwarp();
+      mma_commit(&S.done);  // fires when nothing issued here is in flight
+      mbar_wait(&S.done, 0, kErrMma);
     }
     __syncwarp();
-    if (elect_one()) mma_commit(&S.done);  // fires when nothing issued here is in flight
-    __syncwarp();
-    mbar_wait(&S.done, 0, kErrMma);
   } else {
-    // ---- logits: lane i and i + 16 hold hi and lo of head 16 w + i % 16; after the exchange
-    //      lane i has the head's rows 0-31 of the chunk and lane i + 16 its rows 32-63 ----
+    // ---- logits: thread t of warp w has rows 8 i + 2 (t % 4), + 1 of the chunk for heads
+    //      16 w + t / 4 and that + 8, hi and lo from the two halves of the warp's lanes ----
     const uint32_t lane_base = tmem + ((uint32_t)(32 * warp) << 16);
-    const int hi_half = lane >> 4, head = 16 * warp + (lane & 15);
-    float* zrow = P.z + ((size_t)x.stream * kHg + head) * P.z_rows + 32 * hi_half;
-    float m = -INFINITY, sum = 0.f;
+    const int quad = lane & 3, hq = 16 * warp + (lane >> 2);
+    float m[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+    float* const zt = P.z + ((size_t)x.stream * P.z_tiles) * kTile;
+    uint8_t* const stage = base + kOffZ;
     bool ok = true;
 #pragma unroll 1
-    for (int it = 0; it < n && ok; ++it) {
+    for (int it = 0; it < n; ++it) {
       const int j = x.c0 + it, slot = it & 1, rs = it % kRing;
-      ok = __all_sync(0xffffffffu, mbar_wait(&S.s_full[slot], (uint32_t)(it >> 1) & 1, kErrRead));
+      ok = mbar_wait(&S.s_full[slot], (uint32_t)(it >> 1) & 1, kErrRead);
+      if (tid == 0) bulk_store_wait_read();  // the staged tile of the chunk before has left
+      ok = all_ok(ok);  // the four warps leave together
       if (!ok) break;
       tc_fence_after();
-      uint32_t v[64];
-      tmem_ld_32x32b_x64(lane_base + 64 * slot, v);
+      uint32_t hi[32], lo[32];
+      tmem_ld_16x256b_x8(lane_base + 64 * slot, hi);
+      tmem_ld_16x256b_x8(lane_base + (16u << 16) + 64 * slot, lo);
       tmem_ld_wait();
-      const uint32_t live = S.ring.mask[rs][hi_half];
+      const uint32_t live[2] = {S.ring.mask[rs][0], S.ring.mask[rs][1]};
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&S.ring.free[rs]);
         mbar_arrive(&S.s_free[slot]);
       }
-      float z[32], cm = -INFINITY;
+      float cm[2] = {-INFINITY, -INFINITY};
+      float* const z = reinterpret_cast<float*>(hi);
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const float give = __uint_as_float(hi_half ? v[c] : v[32 + c]);
-        const float keep = __uint_as_float(hi_half ? v[32 + c] : v[c]);
-        const float got = __shfl_xor_sync(0xffffffffu, give, 16);
-        z[c] = (live >> c) & 1u ? (keep + got) * P.scale2 : -INFINITY;
-        cm = fmaxf(cm, z[c]);
+      for (int i = 0; i < 32; ++i) {
+        const int row = 8 * (i >> 2) + 2 * quad + (i & 1), h = (i >> 1) & 1;
+        z[i] = (live[row >> 5] >> (row & 31)) & 1u
+                   ? (__uint_as_float(hi[i]) + __uint_as_float(lo[i])) * P.scale2
+                   : -INFINITY;
+        cm[h] = fmaxf(cm[h], z[i]);
       }
       if (j < x.l.nc) {
-        float4* dst = reinterpret_cast<float4*>(zrow + (size_t)kRows * j);
+        // tile [head][64 rows]; the 32-byte segments of a head are permuted by head % 8, so that
+        // eight heads' stores fall into distinct banks
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          dst[c] = make_float4(z[4 * c], z[4 * c + 1], z[4 * c + 2], z[4 * c + 3]);
+        for (int i = 0; i < 16; ++i) {
+          const int head = hq + 8 * (i & 1), seg = (i >> 1) ^ (head & 7);
+          *reinterpret_cast<float2*>(stage + head * 256 + seg * 32 + quad * 8) =
+              make_float2(z[2 * i], z[2 * i + 1]);
+        }
+        fence_proxy_async_smem();
       }
-      const float mn = fmaxf(m, cm);
-      if (mn != -INFINITY) {
-        float s4[4] = {0.f, 0.f, 0.f, 0.f};
+      bar_readers();
+      if (tid == 0 && j < x.l.nc) bulk_store(zt + (size_t)j * kTile, stage, kTile * 4);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) s4[c & 3] += exp2f(z[c] - mn);
-        sum = sum * exp2f(m - mn) + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
-        m = mn;
+      for (int h = 0; h < 2; ++h) {
+        const float mn = fmaxf(m[h], cm[h]);
+        if (mn != -INFINITY) {
+          float s2[2] = {0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s2[i & 1] += ex2(z[4 * (i >> 1) + 2 * h + (i & 1)] - mn);
+          sum[h] = sum[h] * ex2(m[h] - mn) + (s2[0] + s2[1]);
+          m[h] = mn;
+        }
       }
     }
-    // the two halves of the head
-    const float om = __shfl_xor_sync(0xffffffffu, m, 16), os = __shfl_xor_sync(0xffffffffu, sum, 16);
-    const float M = fmaxf(m, om);
-    float t = 0.f;
-    if (M != -INFINITY) t = sum * exp2f(m - M) + os * exp2f(om - M);
-    if (hi_half == 0) {
-      float* pp = P.part + ((size_t)x.stream * P.nsplit + x.split) * (2 * kHg);
-      pp[head] = M;
-      pp[kHg + head] = t;
+    // the four threads of a head
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float M = m[h];
+      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 1));
+      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 2));
+      float t = m[h] == -INFINITY ? 0.f : sum[h] * ex2(m[h] - M);
+      if (sum[h] != sum[h]) t = sum[h];  // a NaN stays one
+      t += __shfl_xor_sync(0xffffffffu, t, 1);
+      t += __shfl_xor_sync(0xffffffffu, t, 2);
+      if (quad == 0) {
+        float* pp = P.part + ((size_t)x.stream * P.nsplit + x.split) * (2 * kHg);
+        pp[hq + 8 * h] = M;
+        pp[kHg + hq + 8 * h] = t;
+      }
     }
+    if (tid == 0) bulk_store_wait();
   }
   tc_fence_before();
   __syncthreads();
@@ -231,59 +262,79 @@ __device__ __forceinline__ float denominator(const Params& P, int bt, int h) {
   const float* pp = P.part + (size_t)(bt * P.G + g) * P.nsplit * (2 * kHg) + hh;
   const float zs = P.a.sink ? P.a.sink[h] * 1.44269504088896341f : -INFINITY;
   float M = zs;
+#pragma unroll 4
   for (int s = 0; s < P.nsplit; ++s) M = fmaxf(M, pp[s * 2 * kHg]);
   if (M == -INFINITY) return INFINITY;  // no row: every weight is 0
   float t = zs == -INFINITY ? 0.f : exp2f(zs - M);
+#pragma unroll 4
   for (int s = 0; s < P.nsplit; ++s) {
-    const float m = pp[s * 2 * kHg];
-    if (m != -INFINITY) t = fmaf(pp[s * 2 * kHg + kHg], exp2f(m - M), t);
+    const float m = pp[s * 2 * kHg], l = pp[s * 2 * kHg + kHg];
+    if (m != -INFINITY) t = fmaf(l, exp2f(m - M), t);
   }
   return M + log2f(t);
 }
 
-// sum over the heads of 2^(z - L) for row `row` of query bt; L in shared memory
-__device__ __forceinline__ float weight_of(const Params& P, int bt, int64_t row, const float* L) {
+constexpr int kRedThreads = 256;
+constexpr int kParts = 4;                      // threads per row, each a quarter of the heads
+constexpr int kRedRows = kRedThreads / kParts;  // 64: one tile of z
+
+// The sum over all heads of 2^(z - L) for row `row` of query bt, by four threads with a
+// quarter of each group's heads each; all four get it (summed in a fixed order). L and `part`
+// are shared arrays of H and kRedThreads floats; the whole block calls.
+__device__ __forceinline__ float weight_of(const Params& P, int bt, int64_t row, bool in,
+                                           const float* L, float* part) {
+  const int p = threadIdx.x / kRedRows, r = threadIdx.x % kRedRows;
   float s = 0.f;
-  for (int g = 0; g < P.G; ++g) {
-    const float* z = P.z + (size_t)(bt * P.G + g) * kHg * P.z_rows + row;
+  if (in) {
+    for (int g = 0; g < P.G; ++g) {
+      const float* z = P.z + ((size_t)(bt * P.G + g) * P.z_tiles + row / kRows) * kTile;
+      const int c = (int)(row % kRows);
 #pragma unroll 16
-    for (int h = 0; h < kHg; ++h) s += exp2f(z[(size_t)h * P.z_rows] - L[g * kHg + h]);
+      for (int i = 0; i < kHg / kParts; ++i) {
+        const int h = p * (kHg / kParts) + i;
+        s += ex2(z[h * kRows + (((c >> 3) ^ (h & 7)) << 3) + (c & 7)] - L[g * kHg + h]);
+      }
+    }
   }
-  return s;
+  part[threadIdx.x] = s;
+  __syncthreads();
+  const float sum = (part[r] + part[kRedRows + r]) + (part[2 * kRedRows + r] + part[3 * kRedRows + r]);
+  __syncthreads();
+  return sum;
 }
 
-constexpr int kRedThreads = 256;
-
 __global__ void __launch_bounds__(kRedThreads) k_mass_dense(const __grid_constant__ Params P) {
-  extern __shared__ float L[];  // [H]
+  extern __shared__ float sm[];
+  float *part = sm, *L = sm + kRedThreads;  // [H]
   const int b = blockIdx.y;
-  const int64_t e = (int64_t)blockIdx.x * kRedThreads + threadIdx.x;
-  const bool in = e < P.a.n_cap;
-  const float old = in ? P.acc[(size_t)b * P.a.n_cap + e] : 0.f;
+  const int64_t e0 = (int64_t)blockIdx.x * kRedRows, e = e0 + threadIdx.x % kRedRows;
+  const bool writer = threadIdx.x < kRedRows && e < P.a.n_cap;
+  const float old = writer ? P.acc[(size_t)b * P.a.n_cap + e] : 0.f;
   pdl_wait();
   float sum = 0.f;
   for (int t = 0; t < P.a.T; ++t) {
     const int bt = b * P.a.T + t;
     const int64_t n_vis = make_list(P.a, P.a.q_pos[bt]).n_vis;
-    if ((int64_t)blockIdx.x * kRedThreads >= n_vis) continue;  // the same for the whole CTA
-    __syncthreads();
+    if (e0 >= n_vis) continue;  // the same for the whole block
     for (int h = threadIdx.x; h < P.a.H; h += kRedThreads) L[h] = denominator(P, bt, h);
     __syncthreads();
-    if (e < n_vis) sum += weight_of(P, bt, e, L);
+    sum += weight_of(P, bt, e, e < n_vis, L, part);  // ends with a barrier: L may be rewritten
   }
-  if (in) P.acc[(size_t)b * P.a.n_cap + e] = fmaf(P.decay, old, sum);
+  if (writer) P.acc[(size_t)b * P.a.n_cap + e] = fmaf(P.decay, old, sum);
 }
 
 __global__ void __launch_bounds__(kRedThreads) k_mass_sparse(const __grid_constant__ Params P) {
-  extern __shared__ float L[];
+  extern __shared__ float sm[];
+  float *part = sm, *L = sm + kRedThreads;
   const int bt = blockIdx.y, b = bt / P.a.T;
-  const int j = blockIdx.x * kRedThreads + threadIdx.x;
+  const int j = blockIdx.x * kRedRows + threadIdx.x % kRedRows;
   const int e = j < P.a.k ? P.a.idx[(size_t)bt * P.a.k + j] : -1;
   pdl_wait();
   for (int h = threadIdx.x; h < P.a.H; h += kRedThreads) L[h] = denominator(P, bt, h);
   __syncthreads();
-  if (e < 0 || e >= P.a.n_cap) return;
-  const float w = weight_of(P, bt, j, L);
+  const bool in = e >= 0 && e < P.a.n_cap;
+  const float w = weight_of(P, bt, j, in, L, part);
+  if (!in || threadIdx.x >= kRedRows) return;
   unsigned long long* at = P.fixed + (size_t)b * P.a.n_cap + e;
   if (w <= 16777216.f) atomicAdd(at, (unsigned long long)__float2ll_rn(w * kFixed));
   else atomicOr(at, kNotFinite);
@@ -312,7 +363,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Plan {
   int nsplit;
-  int64_t z_rows;
+  int64_t z_tiles;
   size_t z_bytes, part_bytes, fixed_bytes, tile_bytes, rope_bytes;
 };
 
@@ -320,8 +371,8 @@ Plan make_plan(const MqaArgs& a) {
   Plan p;
   const size_t streams = (size_t)a.B * a.T * (a.H / kHg);
   p.nsplit = choose_split(a);
-  p.z_rows = ((a.k > 0 ? a.k : a.n_cap) + kRows - 1) / kRows * kRows;
-  p.z_bytes = up256(streams * kHg * (size_t)p.z_rows * sizeof(float));
+  p.z_tiles = ((a.k > 0 ? a.k : a.n_cap) + kRows - 1) / kRows;
+  p.z_bytes = streams * (size_t)p.z_tiles * kTile * sizeof(float);
   p.part_bytes = up256(streams * p.nsplit * 2 * kHg * sizeof(float));
   p.tile_bytes = q_tiles_bytes(a, true);
   p.rope_bytes = q_rope_bytes(a);
@@ -344,7 +395,7 @@ cudaError_t launch_attn_mass(const MqaArgs& a, float decay, float* acc, void* ws
   P.a = a;
   P.G = a.H / kHg;
   P.nsplit = pl.nsplit;
-  P.z_rows = pl.z_rows;
+  P.z_tiles = pl.z_tiles;
   P.z = reinterpret_cast<float*>(w);
   P.part = reinterpret_cast<float*>(w + pl.z_bytes);
   P.fixed = a.k > 0 ? reinterpret_cast<unsigned long long*>(w + pl.z_bytes + pl.part_bytes) : nullptr;
@@ -362,13 +413,13 @@ cudaError_t launch_attn_mass(const MqaArgs& a, float decay, float* acc, void* ws
   if (e != cudaSuccess) return e;
   e = launch(true, kern, dim3((unsigned)(streams * P.nsplit)), dim3(kThreads), smem, st, P);
   if (e != cudaSuccess) return e;
-  const size_t lsm = (size_t)a.H * sizeof(float);
+  const size_t lsm = (size_t)(kRedThreads + a.H) * sizeof(float);
   if (a.k == 0)
     return launch(true, k_mass_dense,
-                  dim3((unsigned)((a.n_cap + kRedThreads - 1) / kRedThreads), (unsigned)a.B),
+                  dim3((unsigned)((a.n_cap + kRedRows - 1) / kRedRows), (unsigned)a.B),
                   dim3(kRedThreads), lsm, st, P);
   e = launch(true, k_mass_sparse,
-             dim3((unsigned)((a.k + kRedThreads - 1) / kRedThreads), (unsigned)(a.B * a.T)),
+             dim3((unsigned)((a.k + kRedRows - 1) / kRedRows), (unsigned)(a.B * a.T)),
              dim3(kRedThreads), lsm, st, P);
   if (e != cudaSuccess) return e;
   const size_t n = (size_t)a.B * a.n_cap;
