@@ -527,74 +527,60 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
   }
 }
 
-// Merge the partials of one head, add the sink, rotate by -t. Warp w takes splits w, w + 8, ..
-// over all 512 dims (a lane 16 of them), so that every load of the block is in flight at once;
-// the eight states are then merged in a fixed order.
+// Merge the partials, add the sink, rotate by -t. A warp per (head, 128 dims), four dims a lane:
+// lane s has split s's maximum and sum, the loads of sixteen splits go out before anything is
+// computed, and no barrier is needed. Every merged value is a sum over the splits in order.
 __global__ void __launch_bounds__(256) k_attn_fp4_combine(const __grid_constant__ Params P) {
-  __shared__ float so[8][kC], sm[8], sl[8];
   const MqaArgs& a = P.a;
-  const int stream = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bt = stream / P.G, g = stream % P.G, ns = P.nsplit;
+  const int lane = threadIdx.x & 31, ns = P.nsplit;
+  const uint32_t w = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int stream = (int)(w / (4 * kHg)), h = (int)(w / 4) % kHg, quarter = (int)(w & 3);
+  const int bt = stream / P.G, g = stream % P.G;
   const float* base = P.part + (size_t)stream * ns * kPartFloats;
+  const float* ob = base + 2 * kHg + quarter * (kHg * 128) + h * 128 + 4 * lane;
+  const float zs = a.sink ? a.sink[g * kHg + h] * 1.44269504088896341f : -INFINITY;
   pdl_wait();
   pdl_trigger();
-  float M = -INFINITY, l = 0.f;
-  float4 o[4];
+  const float m = lane < ns ? base[(size_t)lane * kPartFloats + h] : -INFINITY;
+  const float l = lane < ns ? base[(size_t)lane * kPartFloats + kHg + h] : 0.f;
+  constexpr int kBatch = 16;
+  float4 v[kBatch];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-  for (int s = warp; s < ns; s += 8) {
-    const float* pp = base + (size_t)s * kPartFloats;
-    const float m = pp[h], ls = pp[kHg + h];
-    float4 v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] = *reinterpret_cast<const float4*>(pp + 2 * kHg + i * (kHg * 128) + h * 128 + 4 * lane);
-    if (m == -INFINITY) continue;  // no row
-    const float Mn = fmaxf(M, m), f0 = exp2f(M - Mn), f = exp2f(m - Mn);
-    M = Mn;
-    l = l * f0 + ls * f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[i].x = o[i].x * f0 + v[i].x * f;
-      o[i].y = o[i].y * f0 + v[i].y * f;
-      o[i].z = o[i].z * f0 + v[i].z * f;
-      o[i].w = o[i].w * f0 + v[i].w * f;
-    }
+  for (int s = 0; s < kBatch; ++s)
+    if (s < ns) v[s] = *reinterpret_cast<const float4*>(ob + (size_t)s * kPartFloats);
+  const int d = 128 * quarter + 4 * lane;
+  float2 c0 = make_float2(1.f, 0.f), c1 = c0;  // of +t
+  if (d >= kNope) {
+    c0 = P.rope[(size_t)bt * 32 + ((d - kNope) >> 1)];
+    c1 = P.rope[(size_t)bt * 32 + ((d - kNope) >> 1) + 1];
   }
+  const float M = fmaxf(warp_max(m), zs);
+  const float f = m == -INFINITY ? 0.f : exp2f(m - M);
+  float den = warp_sum(f * l);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](const float4& x, float fs) {
+    o.x = fmaf(x.x, fs, o.x);
+    o.y = fmaf(x.y, fs, o.y);
+    o.z = fmaf(x.z, fs, o.z);
+    o.w = fmaf(x.w, fs, o.w);
+  };
 #pragma unroll
-  for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(&so[warp][128 * i + 4 * lane]) = o[i];
-  if (lane == 0) {
-    sm[warp] = M;
-    sl[warp] = l;
-  }
-  const int d = 2 * threadIdx.x;
-  float2 cs = make_float2(1.f, 0.f);  // of +t
-  if (d >= kNope) cs = P.rope[(size_t)bt * 32 + ((d - kNope) >> 1)];
-  const float zs = a.sink ? a.sink[g * kHg + h] * 1.44269504088896341f : -INFINITY;
-  __syncthreads();
-  M = zs;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) M = fmaxf(M, sm[i]);
-  float den = 0.f, u = 0.f, v = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (sm[i] != -INFINITY) {
-      const float f = exp2f(sm[i] - M);
-      den = fmaf(sl[i], f, den);
-      u = fmaf(so[i][d], f, u);
-      v = fmaf(so[i][d + 1], f, v);
-    }
-  }
+  for (int s = 0; s < kBatch; ++s)
+    if (s < ns) add(v[s], __shfl_sync(0xffffffffu, f, s));
+#pragma unroll 4
+  for (int s = kBatch; s < ns; ++s)
+    add(*reinterpret_cast<const float4*>(ob + (size_t)s * kPartFloats), __shfl_sync(0xffffffffu, f, s));
+  float r = 0.f;
   if (den != 0.f) {  // a NaN stays one
     den += zs == -INFINITY ? 0.f : exp2f(zs - M);
-    u /= den;
-    v /= den;
+    r = 1.f / den;
   }
-  const float ur = u * cs.x + v * cs.y, vr = v * cs.x - u * cs.y;
-  __nv_bfloat16* out =
-      static_cast<__nv_bfloat16*>(a.out) + ((size_t)bt * a.H + g * kHg + h) * kC + d;
-  *reinterpret_cast<__nv_bfloat162*>(out) = __floats2bfloat162_rn(ur, vr);
+  o.x *= r, o.y *= r, o.z *= r, o.w *= r;
+  __nv_bfloat162 out[2] = {
+      __floats2bfloat162_rn(o.x * c0.x + o.y * c0.y, o.y * c0.x - o.x * c0.y),
+      __floats2bfloat162_rn(o.z * c1.x + o.w * c1.y, o.w * c1.x - o.z * c1.y)};
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) +
+                            ((size_t)bt * a.H + g * kHg + h) * kC + d) = *reinterpret_cast<uint2*>(out);
 }
 
 // CTAs per stream: as many as fill the SMs, at most one per chunk of the longest list, at
@@ -644,7 +630,7 @@ cudaError_t launch_attn_fp4(const MqaArgs& a, void* ws, size_t ws_bytes, cudaStr
   const int grid = P.items < device_sm_count() ? P.items : device_sm_count();
   e = launch(true, k_attn_fp4, dim3((unsigned)grid), dim3(kThreads), smem, st, P);
   if (e != cudaSuccess || P.nsplit == 1) return e;
-  return launch(true, k_attn_fp4_combine, dim3((unsigned)streams, kHg), dim3(256), 0, st, P);
+  return launch(true, k_attn_fp4_combine, dim3((unsigned)(streams * kHg / 2)), dim3(256), 0, st, P);
 }
 
 cudaError_t attn_fp4_device_error(int* code) {

@@ -114,8 +114,12 @@ __device__ __forceinline__ int64_t item_pos(const MqaArgs& a, int w, int G, int 
   return a.q_pos[(uint32_t)w / ((uint32_t)nsplit * (uint32_t)G)];
 }
 
-// Resolved addresses of kRing chunks (0: masked row), their masks of valid rows and what they
-// hold.
+// What a masked row is read from: zero codes and zero bf16 values, so that the gather's loads
+// need no predicate.
+static __device__ __align__(16) uint8_t g_zero_row[kC * 2];
+
+// Resolved addresses of kRing chunks (masked rows: g_zero_row), their masks of valid rows and
+// what they hold.
 enum Kind : uint32_t { kWindow = 0, kCache = 1, kEnd = 2 };  // kEnd: no further chunk
 struct AddrRing {
   uint64_t src[kRing][kRows];
@@ -169,6 +173,7 @@ __device__ __forceinline__ bool resolve_rows(RowBatch& rb, const MqaArgs& a, con
                                              uint32_t& it, AddrRing& ring, int code) {
   const int lane = threadIdx.x & 31;
   constexpr uint32_t kRowBytes = kFmt == kFp4 ? kFp4RowBytes : kC * 2;
+  const uint64_t zero_row = reinterpret_cast<uint64_t>(g_zero_row);
   for (int j0 = x.c0; j0 < x.c1; j0 += kRing) {
     if (j0 > x.c0) rb.lookup(a, x, j0);
     const int n = min(kRing, x.c1 - j0);
@@ -213,7 +218,7 @@ __device__ __forceinline__ bool resolve_rows(RowBatch& rb, const MqaArgs& a, con
         return false;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        ring.src[rs][32 * h + lane] = src[h];
+        ring.src[rs][32 * h + lane] = src[h] != 0 ? src[h] : zero_row;
         const uint32_t m = __ballot_sync(0xffffffffu, src[h] != 0);
         if (lane == 0) ring.mask[rs][h] = m;
       }
@@ -266,10 +271,10 @@ __device__ __forceinline__ uint4 widen8(uint32_t w, __half2 scale) {
   return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
-// 2^E of an exponent byte as f16x2, E clamped to the format's [-14, 13].
+// 2^E of an exponent byte as f16x2. The format holds E to [-14, 13]; the five bits of E + 15 are
+// all that is used of any other byte.
 __device__ __forceinline__ __half2 scale_h2(uint32_t ex) {
-  const uint32_t s = min(max(ex, 113u), 140u) - 112u;  // E + 15
-  const uint32_t u = (s << 10) | (s << 26);
+  const uint32_t u = ((ex - 112u) & 31u) * 0x04000400u;
   return *reinterpret_cast<const __half2*>(&u);
 }
 
@@ -290,33 +295,33 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
 // quarter more time went into waiting for instructions.
 constexpr int kGatherWarps = 9;
 
+__device__ __forceinline__ void st_shared(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
 struct Codes {
   uint4 raw[4];
   uint32_t ex[4];
-  __device__ __forceinline__ void load(const uint64_t* src, int atom) {
-    const int lane = threadIdx.x & 31, u = lane & 1;
+  // off: the lane's byte offset in a row's codes; exo: its exponent's
+  __device__ __forceinline__ void load(const uint64_t* src, int off, int exo) {
+    const uint64_t* p = src + ((threadIdx.x & 31) >> 1);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint8_t* p = reinterpret_cast<const uint8_t*>(src[(lane >> 1) + 16 * i]);
-      raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      ex[i] = 127;
-      if (p != nullptr) {
-        raw[i] = __ldg(reinterpret_cast<const uint4*>(p + 32 * atom + 16 * u));
-        ex[i] = __ldg(p + kFp4Exps + 2 * atom + u);
-      }
+      const uint8_t* row = reinterpret_cast<const uint8_t*>(p[16 * i]);
+      raw[i] = __ldg(reinterpret_cast<const uint4*>(row + off));
+      ex[i] = __ldg(row + exo);
     }
   }
-  __device__ __forceinline__ void store(uint8_t* dst) {
-    const int lane = threadIdx.x & 31, u = lane & 1;
-    uint8_t* at = dst + (lane >> 1) * 128;
-    const uint32_t r7 = (lane >> 1) & 7;
+  // at: the lane's first row in the atom; sw: its swizzled 16-byte pieces
+  __device__ __forceinline__ void store(uint32_t at, const uint32_t (&sw)[4]) {
 #pragma unroll 2
     for (int i = 0; i < 4; ++i, at += 16 * 128) {
       const __half2 s = scale_h2(ex[0]);
       const uint32_t w[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<uint4*>(at + (((4 * u + k) ^ r7) << 4)) = widen8(w[k], s);
+      for (int k = 0; k < 4; ++k) st_shared(at + sw[k], widen8(w[k], s));
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
         raw[k] = raw[k + 1];
@@ -331,24 +336,27 @@ struct Halves {  // bf16 values of rows first .. first + 31
   uint4 raw[8];
   __device__ __forceinline__ void load(const uint64_t* src, int offset, int first) {
     const int lane = threadIdx.x & 31;
+    const uint64_t* p = src + first + (lane >> 3);
+    const uint32_t off = offset + 16 * (lane & 7);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint8_t* p = reinterpret_cast<const uint8_t*>(src[first + (lane >> 3) + 4 * i]);
-      raw[i] = p != nullptr ? __ldg(reinterpret_cast<const uint4*>(p + offset + 16 * (lane & 7)))
-                            : make_uint4(0u, 0u, 0u, 0u);
-    }
+    for (int i = 0; i < 8; ++i)
+      raw[i] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(p[4 * i]) + off));
   }
-  __device__ __forceinline__ void store(uint8_t* dst, int first) {
+  __device__ __forceinline__ void store(uint32_t atom, int first) {
     const int lane = threadIdx.x & 31;
+    const uint32_t r0 = first + (lane >> 3), c = lane & 7;
+    // rows r0 + 4 i: even i share a swizzle, and so do odd ones
+    uint32_t at = atom + r0 * 128;
+    const uint32_t sw0 = (c ^ (r0 & 7)) << 4, sw1 = 512 + ((c ^ ((r0 + 4) & 7)) << 4);
 #pragma unroll 1
-    for (int i = 0; i < 8; i += 2) {
+    for (int i = 0; i < 8; i += 2, at += 1024) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         uint4 o = raw[k];
         if constexpr (kFmt == kFp4)
           o = make_uint4(bf16x2_to_f16x2(o.x), bf16x2_to_f16x2(o.y), bf16x2_to_f16x2(o.z),
                          bf16x2_to_f16x2(o.w));
-        *reinterpret_cast<uint4*>(dst + sw128(first + (lane >> 3) + 4 * (i + k), lane & 7)) = o;
+        st_shared(at + (k ? sw1 : sw0), o);
       }
 #pragma unroll
       for (int k = 0; k < 6; ++k) raw[k] = raw[k + 2];
@@ -425,7 +433,8 @@ __device__ __forceinline__ void gather_loop(uint8_t* kv, int gw, AddrRing& ring,
     __syncwarp();
     if (lane == 0) mbar_arrive(&ring.free[it % kRing]);
   };
-  auto dst_of = [&](uint32_t it) { return kv + ((it % kBufs) * kAtoms + atom) * kAtomBytes; };
+  const uint32_t kv0 = smem_u32(kv) + atom * kAtomBytes;
+  auto dst_of = [&](uint32_t it) { return kv0 + (it % kBufs) * (kAtoms * kAtomBytes); };
   auto buffer = [&](uint32_t it) {
     return wait(&free[(it % kBufs) * kFree + atom / (kAtoms / kFree)], ((it / kBufs) & 1) ^ 1,
                 code + 1);
@@ -438,14 +447,18 @@ __device__ __forceinline__ void gather_loop(uint8_t* kv, int gw, AddrRing& ring,
   uint32_t it = 0, kind = address(0);
   if (kFmt == kFp4 && !last) {
     Codes v;
+    const int u = lane & 1, r = lane >> 1, off = 32 * atom + 16 * u, exo = kFp4Exps + 2 * atom + u;
+    uint32_t sw[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sw[k] = r * 128 + (((4 * u + k) ^ (r & 7)) << 4);
     if (kind == kCache) {
-      v.load(ring.src[0], atom);
+      v.load(ring.src[0], off, exo);
       read(0);
     }
     while (kind != kEnd) {
       if (kind == kCache) {
         if (!buffer(it)) return;
-        v.store(dst_of(it));
+        v.store(dst_of(it), sw);
         publish(it);
       } else {  // window rows, in two halves
         Halves<kFmt> h0, h1;
@@ -459,7 +472,7 @@ __device__ __forceinline__ void gather_loop(uint8_t* kv, int gw, AddrRing& ring,
       }
       kind = address(++it);
       if (kind == kCache) {
-        v.load(ring.src[it % kRing], atom);
+        v.load(ring.src[it % kRing], off, exo);
         read(it);
       }
     }
