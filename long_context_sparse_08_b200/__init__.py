@@ -267,12 +267,23 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_RAW_STREAM = None
+
+
 def _stream(stream) -> Optional[int]:
+    """Handle of `stream`, by default the current device's current stream (torch's raw getter:
+    building a Stream object takes 3 us, more than the rest of a binding call)."""
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
+    global _RAW_STREAM
+    if _RAW_STREAM is None:
+        import torch
 
-    return torch.cuda.current_stream().cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        device = torch.cuda.current_device
+        _RAW_STREAM = (lambda: raw(device())) if raw is not None else \
+            (lambda: torch.cuda.current_stream().cuda_stream)
+    return _RAW_STREAM()
 
 
 def make_params(m=4, overlap=1, c=512, rope_dims=64, rope_base=10000.0, rms_eps=1e-6,

@@ -621,8 +621,8 @@ cudaError_t launch_attn_fp4(const MqaArgs& a, void* ws, size_t ws_bytes, cudaStr
   P.scale2 = a.scale * 1.44269504088896341f;
   const int64_t streams = (int64_t)a.B * a.T * P.G;
   const size_t smem = 1024 + kOffEnd + sizeof(Smem);
-  cudaError_t e = cudaFuncSetAttribute(k_attn_fp4, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(k_attn_fp4, (int)smem, allowed);
   if (e != cudaSuccess) return e;
   e = launch_q_tiles(a, false, w, w + q_tiles_bytes(a, false), st);
   if (e != cudaSuccess) return e;

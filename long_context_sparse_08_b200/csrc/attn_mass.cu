@@ -407,7 +407,8 @@ cudaError_t launch_attn_mass(const MqaArgs& a, float decay, float* acc, void* ws
   const int64_t streams = (int64_t)a.B * a.T * P.G;
   auto kern = a.fp4 ? k_mass_logits<kFp4> : k_mass_logits<kBf16>;
   const size_t smem = 1024 + kOffEnd + sizeof(Smem);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> allowed[2];
+  cudaError_t e = allow_smem(kern, (int)smem, allowed[a.fp4]);
   if (e != cudaSuccess) return e;
   e = launch_q_tiles(a, true, tiles, tiles + pl.tile_bytes, st);
   if (e != cudaSuccess) return e;

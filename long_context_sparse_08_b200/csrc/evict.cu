@@ -16,6 +16,7 @@
 // hand beat a cluster of eight per request (18 to 40 us: seven cluster barriers and sums
 // through distributed shared memory) and a CTA that read the keys from L2 in every pass (26 us).
 #include "common.cuh"
+#include "host_util.cuh"
 #include "internal.h"
 
 namespace csa {
@@ -304,8 +305,8 @@ cudaError_t launch_evict(const EvictArgs& a, void* ws, cudaStream_t st) {
   auto kern = own ? (fits ? k_evict_select<true, true> : k_evict_select<true, false>)
                   : (fits ? k_evict_select<false, true> : k_evict_select<false, false>);
   const size_t smem = fits ? (size_t)a.max_pages * sizeof(uint32_t) : 0;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kSmemKeys * (int)sizeof(uint32_t));
+  static std::atomic<uint64_t> allowed[4];
+  e = allow_smem(kern, kSmemKeys * (int)sizeof(uint32_t), allowed[2 * own + fits]);
   if (e != cudaSuccess) return e;
   return launch(own, kern, dim3((unsigned)a.B), dim3(kThreads), smem, st, a, keys);
 }

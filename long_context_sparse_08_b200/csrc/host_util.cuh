@@ -4,6 +4,9 @@
 
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
+#include <stdint.h>
+
+#include <atomic>
 
 namespace csa {
 
@@ -19,6 +22,20 @@ inline int device_sm_count() {
     return v;
   }();
   return n;
+}
+
+// Allows `kernel` `bytes` of dynamic shared memory on the current device; the runtime is asked
+// once per device (`done`, one word per kernel, remembers which).
+template <typename Kernel>
+inline cudaError_t allow_smem(Kernel kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // cuTensorMapEncodeTiled from the driver (nullptr if the driver does not provide it).
