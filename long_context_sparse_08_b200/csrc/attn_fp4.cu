@@ -60,10 +60,9 @@ enum { kErrRing = 211, kErrGather = 212, kErrMma = 214, kErrSoftmax = 215 };
 
 struct Smem {
   AddrRing ring;
-  uint64_t kv_full[kBuf], kv_free[kBuf * kFree], s_full[kBuf], p_full[kBuf], vote[kBuf], q_full, done[2];
+  uint64_t kv_full[kBuf], kv_free[kBuf * kFree], s_full[kBuf], p_full[kBuf], q_full, done[2];
   uint32_t tmem_slot;
-  uint32_t need[4][4];  // [chunk % 4][softmax warp]: a head of the warp raised its maximum
-  float alpha[2][kHg], fin[kHg];
+  float alpha[kHg], fin[kHg];
 };
 
 struct Params {
@@ -88,8 +87,17 @@ __device__ __forceinline__ bool all_softmax(bool ok) {
       : "memory");
   return res != 0;
 }
-// A wait of one softmax warp. No barrier of the four warps follows it inside the chunk loop,
-// so a warp whose wait gives up leaves the others to their own limits.
+// Barrier of the four warps; the number of threads that vote.
+__device__ __forceinline__ uint32_t count_softmax(bool vote) {
+  uint32_t n;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.popc.u32 %0, 1, 128, q;\n\t}"
+      : "=r"(n)
+      : "r"((uint32_t)vote)
+      : "memory");
+  return n;
+}
+// A wait of one softmax warp. One that gives up is told to the others by the next vote.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, kErrSoftmax));
 }
@@ -147,7 +155,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
         for (int k = 0; k < kFree; ++k) mbar_init(&S.kv_free[i * kFree + k], 1);
         mbar_init(&S.s_full[i], 1);
         mbar_init(&S.p_full[i], 4);
-        mbar_init(&S.vote[i], 4);
       }
       mbar_init(&S.q_full, 1);
       for (int i = 0; i < 2; ++i) mbar_init(&S.done[i], 1);
@@ -215,9 +222,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
         const uint32_t end = it + (uint32_t)(x.c1 - x.c0);
         for (; ok && it != end; ++it) {
           const uint32_t slot = it & 1, ph = (it >> 1) & 1;
-          // the softmax of chunk it - 2 has read this S tile once it published P
-          ok = (it < 2 || mbar_wait(&S.p_full[slot], ph ^ 1, kErrMma)) &&
-               mbar_wait(&S.kv_full[slot], ph, kErrMma);
+          // The buffer was given back by the products of chunk it - 2, so the softmax has read
+          // this S tile, too.
+          ok = mbar_wait(&S.kv_full[slot], ph, kErrMma);
           if (!ok) break;
           tc_fence_after();
           const uint64_t dk = dk0 + (uint64_t)(slot * (kSlotKV >> 4));
@@ -285,10 +292,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
       const uint32_t it0 = it, n = (uint32_t)(x.c1 - x.c0);
       float mu[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
 #pragma unroll 1
-      for (; it - it0 < n && ok; ++it) {
+      for (; it - it0 < n; ++it) {  // (left by the vote alone, so by all four warps)
         const uint32_t slot = it % kBuf, rs = it % kRing;
-        ok = wait_warp(&S.s_full[slot], (it / kBuf) & 1);
-        if (!ok) break;
+        ok = wait_warp(&S.s_full[slot], (it / kBuf) & 1) && ok;
         tc_fence_after();
         uint32_t sv[32];
         tmem_ld_16x256b_x8(lane_base + kColS + 64 * slot, sv);
@@ -327,15 +333,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
           lsum[h] *= al[h];
           mref[h] = mu[h] == -INFINITY ? 0.f : mu[h];
         }
-        // the warps tell one another whether a maximum was raised, and look once P is computed
+        // One barrier of the four warps per chunk: the whole warp votes where a maximum was
+        // raised, a single lane where the warp's wait gave up, and all leave together then.
         const bool raised = __any_sync(0xffffffffu, (al[0] != 1.f || al[1] != 1.f) && it != it0);
-        if (quad == 0) {
-          S.alpha[it & 1][hq] = al[0];
-          S.alpha[it & 1][hq + 8] = al[1];
+        if (raised && quad == 0) {
+          S.alpha[hq] = al[0];
+          S.alpha[hq + 8] = al[1];
         }
-        if (lane == 0) S.need[it & 3][warp] = raised ? 1u : 0u;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.vote[it & 1]);
+        if (!raised && quad == 0 && it != it0) S.alpha[hq] = S.alpha[hq + 8] = 1.f;
+        const uint32_t votes = count_softmax(ok ? raised : lane == 0);
+        if (votes & 31u) {
+          ok = false;
+          break;
+        }
         // p = 2^(s * scale2 - m), paired into f16x2
         float l4[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
@@ -349,13 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
         }
         lsum[0] += l4[0][0] + l4[0][1];
         lsum[1] += l4[1][0] + l4[1][1];
-        ok = wait_warp(&S.vote[it & 1], (it >> 1) & 1);
-        if (!ok) break;
-        if ((S.need[it & 3][0] | S.need[it & 3][1] | S.need[it & 3][2] | S.need[it & 3][3]) != 0) {
+        if (votes != 0) {
           // rare: scale this warp's dims of O^T by alpha once the previous chunk's products are
-          // done (a chunk's alpha is rewritten two chunks later, after all warps published P)
+          // done. A wait that gives up here shows in the next vote.
           ok = wait_warp(chunk_done(it - 1), ((it - 1) / kBuf) & 1);
-          if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
           for (int cg = 0; cg < 16; ++cg) {  // 4 slices x 4 groups of 16 heads
@@ -365,15 +372,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
             tmem_ld_wait();
 #pragma unroll
             for (int h = 0; h < 16; ++h)
-              o[h] = __float_as_uint(__uint_as_float(o[h]) * S.alpha[it & 1][16 * (cg & 3) + h]);
+              o[h] = __float_as_uint(__uint_as_float(o[h]) * S.alpha[16 * (cg & 3) + h]);
             tmem_st_x16(ta, o);
           }
           tmem_st_wait();
+          count_softmax(false);  // alpha has been read
         }
-        if (it >= kBuf) {  // the P buffer was read by the products of chunk it - 2
-          ok = wait_warp(chunk_done(it), ((it - kBuf) / kBuf) & 1);
-          if (!ok) break;
-        }
+        // (the P buffer was read by the products of chunk it - 2: see S above)
         // K-major tile [head][64 rows]: 8 x 8 pieces of 16-bit values, four a store: column groups
         // 2 c and 2 c + 1 of heads 16w .. 16w + 7 and 16w + 8 .. 16w + 15. Lane l gives the
         // address of row l % 8 of piece l / 8 (heads + 8 in odd pieces).
