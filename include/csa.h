@@ -414,7 +414,7 @@ size_t csa_evict_pages_workspace_size(int32_t B, int32_t max_pages);
 
 /*
  * The CSA layer over the state cache's paged caches: csa_index_topk_paged on `keys`
- * (optionally with BF16 index scores), then the sparse MQA over `kv` (bf16 or mixed rows,
+ * (optionally with BF16 index scores), then the sparse MQA over `kv` (bf16, mixed or 4-bit rows,
  * as csa_sparse_mqa_paged), in one call with the decode chain of csa_forward. io = bf16 for
  * q [B, T, H, c], the window and out; qI (and qI_scale for MXFP4 keys) as for
  * csa_index_topk_paged with keys->fmt; w f32 [B, T, 64]. Both pools

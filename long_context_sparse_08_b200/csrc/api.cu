@@ -330,10 +330,10 @@ size_t csa_workspace_size(const csa_params* p, int32_t entry, csa_dtype kdt, int
     case CSA_WS_HCA_MQA:
       m.k = 0;
       return round_up(attn_bytes(m, fp4));
-    case CSA_WS_FORWARD: {  // kdt names the keys here: room for the attention of any KV format
-      const size_t any = std::max(attn_bytes(m, false), attn_bytes(m, true));
-      return scores_bytes(B, T, N_cap) + topk_ws + round_up(any) + qhat_bytes(p, B, T, N_cap);
-    }
+    case CSA_WS_FORWARD:  // kdt names the keys here: room for the attention of any KV format
+      return scores_bytes(B, T, N_cap) + topk_ws +
+             std::max(round_up(attn_bytes(m, false)) + qhat_bytes(p, B, T, N_cap),
+                      round_up(attn_bytes(m, true)));
     default:
       fail(CSA_ERR_INVALID_ARG, "unknown workspace entry %d", entry);
       return 0;

@@ -55,6 +55,17 @@ def test_attention_over_4_bit_pages():
         csa.workspace_size(p, csa.CSA_WS_SPARSE_MQA, csa.CSA_MIXED_FP8_BF16, 1, 1, 512)
 
 
+@pytest.mark.parametrize("B,T,N", [(1, 1, 512), (8, 1, 32768), (1, 8192, 16384)])
+def test_forward_workspace_has_room_for_either_attention(B, T, N):
+    """The selection's bytes, then either the bf16 attention with its q_hat (1 KB a head) or the
+    attention over 4-bit rows, which brings its own: their maximum, not their sum."""
+    p = csa.make_params(topk=512)
+    size = lambda entry, kdt: csa.workspace_size(p, entry, kdt, B, T, N)  # noqa: E731
+    either = max(size(csa.CSA_WS_SPARSE_MQA, csa.CSA_BF16) + B * T * p.n_heads * p.c * 2,
+                 size(csa.CSA_WS_SPARSE_MQA, csa.CSA_MIXED_MXFP4_BF16))
+    assert size(csa.CSA_WS_FORWARD, csa.CSA_BF16) == size(csa.CSA_WS_INDEX_TOPK, csa.CSA_BF16) + either
+
+
 def test_writers_of_4_bit_pages():
     L = csa.lib()
     enc = lambda p, kv: L.csa_encode_paged(  # noqa: E731
