@@ -218,6 +218,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
         peek();
         mbar_arrive_expect_tx(&S.q_full, kQBytes);
         bulk_load(base + kOffQ, P.tiles + (size_t)x.stream * kQBytes, kQBytes, &S.q_full);
+        if (w + step < P.items)  // the next tile towards L2: many queries' tiles lie in HBM
+          bulk_prefetch_l2(P.tiles + (size_t)((uint32_t)(w + step) / (uint32_t)P.nsplit) * kQBytes,
+                           kQBytes);
         ok = mbar_wait(&S.q_full, item & 1, kErrMma);
         const uint32_t end = it + (uint32_t)(x.c1 - x.c0);
         for (; ok && it != end; ++it) {
@@ -402,6 +405,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
       }
       // ---- epilogue ----
       pdl_wait();  // the rotation, written beside the tiles
+      // dims d = r, r + 8 of 32 warp + 16 half (r = lane / 4) of the last slice's last two warps
+      float2 rot[2][2];
+      if (warp >= 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          rot[i >> 1][i & 1] =
+              P.rope[(size_t)x.bt * 32 + ((32 * (warp - 2) + 8 * i + (lane >> 2)) >> 1)];
+      }
       const int h0 = (x.stream - x.bt * P.G) * kHg;
       const bool single = P.nsplit == 1;
       float* pp = P.part + ((size_t)x.stream * P.nsplit + x.split) * kPartFloats;
@@ -430,47 +441,52 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
       tc_fence_after();
       if (single) {
         // Per slice of 128 dims, each warp its 32 (two pieces of 16 lanes): pairs of heads become
-        // bf16x2, stored transposed into [head][128 dims] in the P buffers (idle until the next
-        // item's first P, which these warps write), then whole rows of 256 bytes go out.
-        const uint32_t st = smem_u32(base + kOffP);
+        // bf16x2, stored transposed into [head][32 dims] in the warp's quarter of the P buffers
+        // (idle until the next item's first P), then 64 bytes of every head's row go out. The
+        // 16-byte pieces are permuted by head / 2, so that eight heads' fall into distinct banks.
+        const uint32_t st = smem_u32(base + kOffP) + warp * (kHg * 64);
         float f0[8], f1[8];  // of heads 8 i + 2 quad, + 1
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           f0[i] = S.fin[8 * i + 2 * quad];
           f1[i] = S.fin[8 * i + 2 * quad + 1];
         }
+        const int oh = lane >> 2, oc = lane & 3;  // head of eight and 16-byte piece written out
+        const uint8_t* from = base + kOffP + warp * (kHg * 64) + oh * 64 + ((oc ^ (oh >> 1)) << 4);
         uint8_t* out = reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(a.out) +
-                                                  ((size_t)x.bt * a.H + h0) * kC);
+                                                  ((size_t)x.bt * a.H + h0) * kC) +
+                       oh * (kC * 2) + 64 * warp + 16 * oc;
 #pragma unroll 1
-        for (int sl = 0; sl < 4; ++sl) {
-#pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            uint32_t o[32];
+        for (int sl = 0; sl < 4; ++sl, out += 256) {
+          uint32_t o[2][32];
+          if (have) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0u;
-            if (have) {
-              tmem_ld_16x256b_x8(lane_base + ((uint32_t)(16 * half) << 16) + kColO + 64 * sl, o);
-              tmem_ld_wait();
-            }
+            for (int half = 0; half < 2; ++half)
+              tmem_ld_16x256b_x8(lane_base + ((uint32_t)(16 * half) << 16) + kColO + 64 * sl, o[half]);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[0][i] = o[1][i] = 0u;
+          }
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
             // registers 4 i, + 1: heads 8 i + 2 quad, + 1 of dim r = lane / 4; + 2, + 3: of dim r + 8
             float y[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              y[i] = __uint_as_float(o[i]) * ((i & 1) ? f1[i >> 2] : f0[i >> 2]);
-            const int d = 128 * sl + 32 * warp + 16 * half + (lane >> 2);
+              y[i] = __uint_as_float(o[half][i]) * ((i & 1) ? f1[i >> 2] : f0[i >> 2]);
             if (128 * sl + 32 * warp >= kNope) {  // rotation by -t: dims d, d ^ 1 are lanes l, l ^ 4
-              const float2 c0 = P.rope[(size_t)x.bt * 32 + ((d - kNope) >> 1)];
-              const float2 c1 = P.rope[(size_t)x.bt * 32 + ((d + 8 - kNope) >> 1)];
-              const float sg = (d & 1) ? -1.f : 1.f;
+              const float sg = (lane & 4) ? -1.f : 1.f;
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 const float other = __shfl_xor_sync(0xffffffffu, y[i], 4);
-                const float2 c = (i & 2) ? c1 : c0;
+                const float2 c = rot[half][(i >> 1) & 1];
                 y[i] = y[i] * c.x + sg * other * c.y;
               }
             }
             // pieces of 8 dims x 8 heads; the transposed store writes, for head row r of a piece,
-            // its 8 dims: piece 2 i + (dims + 8); 16-byte chunk (32 warp + 16 half) / 8 + dims + 8
+            // its 8 dims: piece 2 i + (dims + 8); 16-byte piece 2 half + dims + 8 of the 64 bytes
+            const int chunk = 2 * half + ((lane >> 3) & 1), r = lane & 7;
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
               uint32_t p[4];
@@ -479,20 +495,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
                 const int e = 4 * (i + (k >> 1)) + 2 * (k & 1);
                 p[k] = pack2<kBf16>(y[e], y[e + 1]);
               }
-              const int head = 8 * (i + (lane >> 4)) + (lane & 7);
-              const int chunk = 4 * warp + 2 * half + ((lane >> 3) & 1);
-              stmatrix_x4_trans(st + head * 256 + ((chunk ^ (head & 7)) << 4), p[0], p[1], p[2], p[3]);
+              stmatrix_x4_trans(st + (8 * (i + (lane >> 4)) + r) * 64 + ((chunk ^ (r >> 1)) << 4), p[0],
+                                p[1], p[2], p[3]);
             }
           }
-          bar_softmax();
+          __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int head = 16 * warp + 2 * i + (lane >> 4), chunk = lane & 15;
-            const uint4 v = *reinterpret_cast<const uint4*>(base + kOffP + head * 256 +
-                                                            ((chunk ^ (head & 7)) << 4));
-            *reinterpret_cast<uint4*>(out + (size_t)head * (kC * 2) + 256 * sl + 16 * chunk) = v;
-          }
-          bar_softmax();
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(out + (size_t)i * (8 * kC * 2)) =
+                *reinterpret_cast<const uint4*>(from + i * (8 * 64));
+          __syncwarp();
         }
         tc_fence_before();
       } else {

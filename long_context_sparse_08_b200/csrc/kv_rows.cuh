@@ -106,8 +106,9 @@ struct Item {
     bt = (int)((uint32_t)stream / (uint32_t)G);
     b = (int)((uint32_t)bt / (uint32_t)a.T);
     l = make_list(a, t);
-    c0 = (int)(((uint64_t)l.n_chunks * (uint32_t)split) / (uint32_t)nsplit);
-    c1 = (int)(((uint64_t)l.n_chunks * (uint32_t)(split + 1)) / (uint32_t)nsplit);
+    const int each = (int)((uint32_t)l.n_chunks / (uint32_t)nsplit), more = l.n_chunks - each * nsplit;
+    c0 = each * split + min(split, more);
+    c1 = c0 + each + (split < more ? 1 : 0);
   }
 };
 __device__ __forceinline__ int64_t item_pos(const MqaArgs& a, int w, int G, int nsplit) {
@@ -395,6 +396,12 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
           smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
+}
+
+__device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(src)),
+               "r"(bytes)
+               : "memory");
 }
 
 __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
