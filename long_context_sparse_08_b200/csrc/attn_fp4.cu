@@ -58,8 +58,17 @@ constexpr uint32_t kColO = 256;  // O^T slice s: 256 + 64 s
 // 216 = 211 + 5: a page id outside the pool
 enum { kErrRing = 211, kErrGather = 212, kErrMma = 214, kErrSoftmax = 215 };
 
+// What the other roles have to know of an item; n = 0 ends the list.
+struct alignas(16) ItemInfo {
+  int stream, bt, w;
+  uint32_t n;  // chunks, at least one (an empty share has one whose rows are all masked)
+};
+constexpr int kItems = 8;  // see the address warp
+
 struct Smem {
   AddrRing ring;
+  ItemInfo info[kItems];
+  uint64_t item_full[kItems];
   uint64_t kv_full[kBuf], kv_free[kBuf * kFree], s_full[kBuf], p_full[kBuf], q_full, done[2];
   uint32_t tmem_slot;
   float alpha[kHg], fin[kHg];
@@ -156,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
         mbar_init(&S.s_full[i], 1);
         mbar_init(&S.p_full[i], 4);
       }
+      for (int i = 0; i < kItems; ++i) mbar_init(&S.item_full[i], 1);
       mbar_init(&S.q_full, 1);
       for (int i = 0; i < 2; ++i) mbar_init(&S.done[i], 1);
       fence_barrier_init();
@@ -165,11 +175,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
   }
   // The q_tiles launch before this one waited for everything earlier on the stream, and this
   // kernel starts after that: only the tiles themselves are waited for, below.
+  int w = blockIdx.x;
   Item x;
-  int64_t t_next = item_pos(a, blockIdx.x, P.G, P.nsplit);
-  x.set(a, blockIdx.x, P.G, P.nsplit, t_next);
   RowBatch rows0;
-  if (warp == 5) rows0.lookup(a, x, x.c0);
+  // a share without rows becomes one chunk without rows
+  auto set_item = [&](int64_t t) {
+    x.set(a, w, P.G, P.nsplit, t);
+    if (x.c1 == x.c0) x.c1 = x.c0 + 1;
+  };
+  if (warp == 5) {
+    set_item(item_pos(a, w, P.G, P.nsplit));
+    rows0.lookup(a, x, x.c0);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -177,31 +194,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
   const uint32_t tmem = S.tmem_slot;
   // Each role walks the CTA's items (one, where streams are split; several for many queries)
   // with its own count of chunks, so the next item's rows are gathered and multiplied while the
-  // last one is finalised.
-  int w = blockIdx.x;
+  // last one is finalised. The address warp works the items out and passes them on: with every
+  // role doing so for itself, the change of item took 1800 cycles.
   uint32_t it = 0;
   bool ok = true;
-  auto peek = [&]() {  // the next item's position, an item ahead of its use
-    if (w + step < P.items) t_next = item_pos(a, w + step, P.G, P.nsplit);
-  };
-  auto advance = [&]() {
-    w += step;
-    if (w >= P.items) return false;
-    x.set(a, w, P.G, P.nsplit, t_next);
-    return true;
-  };
-
   if (warp >= 7) {
     gather_loop<kFp4, kBuf, 1, kFree>(base + kOffKV, warp - 7, S.ring, S.kv_full, S.kv_free,
                                       kErrGather);
   } else if (warp == 5) {
+    // An item is passed on where its first chunk `it` has its place in the ring: chunk it - 4 has
+    // left the softmax, so S of it is done, its buffer was given back by chunk it - 6, and every
+    // role is at most seven items (of a chunk at least) behind.
+    uint32_t item = 0;
+    auto pass = [&](uint32_t n) {
+      if (lane == 0) {
+        S.info[item % kItems] = ItemInfo{x.stream, x.bt, w, n};
+        mbar_arrive(&S.item_full[item % kItems]);
+      }
+      ++item;
+    };
     while (true) {
-      peek();
-      ok = resolve_rows<kFp4>(rows0, a, x, it, S.ring, kErrRing);
-      if (!ok || !advance()) break;
+      const bool more = w + step < P.items;
+      int64_t t_next = 0;
+      if (more) t_next = item_pos(a, w + step, P.G, P.nsplit);
+      ok = resolve_rows<kFp4>(rows0, a, x, it, S.ring, kErrRing,
+                              [&] { pass((uint32_t)(x.c1 - x.c0)); });
+      if (!ok || !more) break;
+      w += step;
+      set_item(t_next);
       rows0.lookup(a, x, x.c0);
     }
-    if (ok) resolve_end(it, S.ring, kErrRing);
+    if (ok) resolve_end(it, S.ring, kErrRing, [&] { pass(0); });
   } else if (warp == 4) {
     // ------------------------------ S ------------------------------
     // One thread runs the whole loop (the votes and branches of a converged warp cost as much as
@@ -215,14 +238,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
       constexpr uint32_t kQBytes = kAtoms * kHg * 128;
       pdl_wait();  // the tiles
       for (uint32_t item = 0;; ++item) {
-        peek();
+        ok = mbar_wait(&S.item_full[item % kItems], (item / kItems) & 1, kErrMma);
+        const ItemInfo info = S.info[item % kItems];
+        if (!ok || info.n == 0) break;
         mbar_arrive_expect_tx(&S.q_full, kQBytes);
-        bulk_load(base + kOffQ, P.tiles + (size_t)x.stream * kQBytes, kQBytes, &S.q_full);
-        if (w + step < P.items)  // the next tile towards L2: many queries' tiles lie in HBM
-          bulk_prefetch_l2(P.tiles + (size_t)((uint32_t)(w + step) / (uint32_t)P.nsplit) * kQBytes,
-                           kQBytes);
+        bulk_load(base + kOffQ, P.tiles + (size_t)info.stream * kQBytes, kQBytes, &S.q_full);
+        if (info.w + step < P.items)  // the next tile towards L2 (an item a stream here)
+          bulk_prefetch_l2(P.tiles + (size_t)(info.stream + step) * kQBytes, kQBytes);
         ok = mbar_wait(&S.q_full, item & 1, kErrMma);
-        const uint32_t end = it + (uint32_t)(x.c1 - x.c0);
+        const uint32_t end = it + info.n;
         for (; ok && it != end; ++it) {
           const uint32_t slot = it & 1, ph = (it >> 1) & 1;
           // The buffer was given back by the products of chunk it - 2, so the softmax has read
@@ -240,8 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
           mma_commit(&S.s_full[slot]);
         }
         // the item's last S has read q_hat before the next one replaces it
-        if (ok && x.c1 > x.c0) ok = mbar_wait(&S.s_full[(it - 1) & 1], ((it - 1) >> 1) & 1, kErrMma);
-        if (!ok || !advance()) break;
+        ok = ok && mbar_wait(&S.s_full[(it - 1) & 1], ((it - 1) >> 1) & 1, kErrMma);
+        if (!ok) break;
       }
       mma_commit(&S.done[0]);  // fires when nothing issued here is in flight
       mbar_wait(&S.done[0], 0, kErrMma);
@@ -254,9 +278,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
       const uint32_t sb = smem_u32(base);
       const uint64_t dv0 = smem_desc(sb + kOffKV, kAtomBytes, 1024, kLayoutSw128);
       const uint64_t dp0 = smem_desc(sb + kOffP, 16, 1024, kLayoutSw128);
-      do {
-        peek();
-        const uint32_t first = it, end = it + (uint32_t)(x.c1 - x.c0);
+      for (uint32_t item = 0; ok; ++item) {
+        ok = mbar_wait(&S.item_full[item % kItems], (item / kItems) & 1, kErrMma);
+        const uint32_t first = it, n = S.info[item % kItems].n, end = it + n;
+        if (!ok || n == 0) break;
         for (; it != end; ++it) {
           const uint32_t slot = it & 1;
           // P says that S is done, that O^T was rescaled where needed, and, of an item's first
@@ -275,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
             mma_commit(&S.kv_free[slot * kFree + sl]);
           }
         }
-      } while (ok && advance());
+      }
       mma_commit(&S.done[1]);
       mbar_wait(&S.done[1], 0, kErrMma);
     }
@@ -290,9 +315,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
     const int quad = lane & 3, hq = 16 * warp + (lane >> 2);
     // fires when every product of chunk i is done (its last slice's)
     auto chunk_done = [&](uint32_t i) { return &S.kv_free[(i % kBuf) * kFree + kFree - 1]; };
-    while (true) {
-      peek();
-      const uint32_t it0 = it, n = (uint32_t)(x.c1 - x.c0);
+    for (uint32_t item = 0;; ++item) {
+      ok = wait_warp(&S.item_full[item % kItems], (item / kItems) & 1) && ok;
+      // the four warps leave together; S.fin has been read before this item writes it
+      ok = all_softmax(ok);
+      const ItemInfo x = S.info[item % kItems];
+      if (!ok || x.n == 0) break;
+      const uint32_t it0 = it, n = x.n;
       float mu[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
 #pragma unroll 1
       for (; it - it0 < n; ++it) {  // (left by the vote alone, so by all four warps)
@@ -415,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
       }
       const int h0 = (x.stream - x.bt * P.G) * kHg;
       const bool single = P.nsplit == 1;
-      float* pp = P.part + ((size_t)x.stream * P.nsplit + x.split) * kPartFloats;
+      float* pp = P.part + (size_t)x.w * kPartFloats;
       if (quad == 0) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -435,8 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
           }
         }
       }
-      if (ok && n > 0) ok = wait_warp(chunk_done(it - 1), ((it - 1) / kBuf) & 1);
-      const bool have = ok && n > 0;
+      const bool have = ok && wait_warp(chunk_done(it - 1), ((it - 1) / kBuf) & 1);
+      ok = have;
       bar_softmax();  // S.fin
       tc_fence_after();
       if (single) {
@@ -531,9 +560,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
         }
         if (lane == 0) bulk_store_wait();
       }
-      // the four warps leave together; S.fin has been read before the next item writes it
-      ok = all_softmax(ok);
-      if (!ok || !advance()) break;
     }
   }
   tc_fence_before();

@@ -134,7 +134,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_mass_logits(const __grid_consta
                                          kErrGather);
   } else if (warp == 5) {
     uint32_t it = 0;
-    if (resolve_rows<kFmt>(rows0, a, x, it, S.ring, kErrRing)) resolve_end(it, S.ring, kErrRing);
+    if (resolve_rows<kFmt>(rows0, a, x, it, S.ring, kErrRing, [] {}))
+      resolve_end(it, S.ring, kErrRing, [] {});
   } else if (warp == 4) {
     if (n > 0 && elect_one()) {  // one thread issues everything (see attn_fp4.cu)
       const uint32_t idS = idesc_f16(kFmt == kFp4 ? 0 : 1, kQRows, kRows);

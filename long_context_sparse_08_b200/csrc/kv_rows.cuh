@@ -168,10 +168,11 @@ struct RowBatch {
 
 // The address warp: the chunks of item x, the first batch already looked up; `it` counts the
 // CTA's chunks. `code`: error code of a wait that gave up; code + 5: a page id outside the pool
-// (an evicted page is masked quietly).
-template <int kFmt>
+// (an evicted page is masked quietly). begin() is called where the item's first chunk has its
+// place in the ring.
+template <int kFmt, class Begin>
 __device__ __forceinline__ bool resolve_rows(RowBatch& rb, const MqaArgs& a, const Item& x,
-                                             uint32_t& it, AddrRing& ring, int code) {
+                                             uint32_t& it, AddrRing& ring, int code, Begin begin) {
   const int lane = threadIdx.x & 31;
   constexpr uint32_t kRowBytes = kFmt == kFp4 ? kFp4RowBytes : kC * 2;
   const uint64_t zero_row = reinterpret_cast<uint64_t>(g_zero_row);
@@ -217,6 +218,7 @@ __device__ __forceinline__ bool resolve_rows(RowBatch& rb, const MqaArgs& a, con
       const uint32_t rs = it % kRing;
       if (!__all_sync(0xffffffffu, mbar_wait(&ring.free[rs], ((it / kRing) & 1) ^ 1, code)))
         return false;
+      if (j == x.c0) begin();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         ring.src[rs][32 * h + lane] = src[h] != 0 ? src[h] : zero_row;
@@ -244,9 +246,11 @@ __device__ __forceinline__ bool resolve_rows(RowBatch& rb, const MqaArgs& a, con
 }
 
 // After the last item: tells the gather warps to stop.
-__device__ __forceinline__ void resolve_end(uint32_t it, AddrRing& ring, int code) {
+template <class Begin>
+__device__ __forceinline__ void resolve_end(uint32_t it, AddrRing& ring, int code, Begin begin) {
   const uint32_t rs = it % kRing;
   if (!__all_sync(0xffffffffu, mbar_wait(&ring.free[rs], ((it / kRing) & 1) ^ 1, code))) return;
+  begin();
   if ((threadIdx.x & 31) == 0) {
     ring.kind[rs] = kEnd;
     mbar_arrive(&ring.full[rs]);
