@@ -626,15 +626,21 @@ __global__ void __launch_bounds__(256) k_attn_fp4_combine(const __grid_constant_
                             ((size_t)bt * a.H + g * kHg + h) * kC + d) = *reinterpret_cast<uint2*>(out);
 }
 
-// CTAs per stream: as many as fill the SMs, at most one per chunk of the longest list, at
-// most kMaxSplit.
+// CTAs per stream: as many as fill the SMs, at most one per chunk of the longest list, at most
+// kMaxSplit, and no more than the largest share needs. With one chunk a CTA the partials (128 KB
+// each, written and read again) can cost more than a second chunk does. One against two chunks a
+// CTA, in us: 80 CTAs with 10 to a stream 14.0 / 15.1, 140 with 10 17.3 / 17.8, 72 with 18 14.2 /
+// 15.1, but 108 with 18 15.9 / 15.6 and 144 with 18 17.3 / 15.9.
 int choose_split(const MqaArgs& a) {
   const int64_t streams = (int64_t)a.B * a.T * (a.H / kHg);
   const int64_t rows = a.k > 0 ? a.k : a.n_cap;
   const int64_t chunks = (rows + kRows - 1) / kRows + ((int64_t)a.n_win + kRows - 1) / kRows;
   int64_t ns = device_sm_count() / (streams > 0 ? streams : 1);
   ns = ns < chunks ? ns : chunks;
-  return (int)(ns < 1 ? 1 : (ns > kMaxSplit ? kMaxSplit : ns));
+  ns = ns < 1 ? 1 : (ns > kMaxSplit ? kMaxSplit : ns);
+  int64_t share = (chunks + ns - 1) / ns;
+  if (share == 1 && ns > 16 && streams * ns > 88) share = 2;
+  return share > 0 ? (int)((chunks + share - 1) / share) : 1;
 }
 
 }  // namespace
