@@ -403,7 +403,9 @@ size_t csa_attn_mass_workspace_size(const csa_params* p, int32_t B, int32_t T, i
  *   evicted int32 [B, max_pages]: the evicted logical pages, ascending, then -1;
  *   counts int32 [B, 3]: kept pages, their entries, evicted pages.
  * Entries keep their numbers, and nothing is moved. On the host, csa_page_alloc_evict gives the
- * evicted pages back to their pool. Workspace: csa_evict_pages_workspace_size.
+ * evicted pages back to their pool. An indexer's key pages are a pool of their own and stay: what
+ * it selects among evicted entries the attention skips, so that fewer than topk rows remain.
+ * Workspace: csa_evict_pages_workspace_size.
  */
 csa_status csa_evict_pages(const csa_params* p, int32_t B, int32_t page_rows, int32_t max_pages,
                            const int64_t* pos, const float* acc, const int32_t* page_table,

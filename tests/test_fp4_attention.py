@@ -90,6 +90,39 @@ def test_evicted_pages_of_bf16_rows_are_masked_quietly():
     assert np.sqrt(((got - ref) ** 2).sum() / (ref ** 2).sum()) <= 5e-3  # the bf16 path's own bound
 
 
+def _poison(P):
+    """NaN in every byte that the queries may not read: rows of the pool that no visible entry
+    has, and window rows outside the last n_win positions."""
+    keep = np.zeros((P.n_pages, P.page_rows), bool)
+    for b in range(P.B):
+        vis = min(int(P.pos[b].max()) // P.m, P.N)
+        e = np.arange(vis) if not P.k else np.unique(P.idx[b].cpu().numpy())
+        e = e[e >= 0]
+        keep[P.table[b, e // P.page_rows], e % P.page_rows] = True
+        rows = np.unique([t for q in P.pos[b] for t in range(max(0, q - P.n_win + 1), q + 1)])
+        at = rows % P.L if P.win_pos0 is None else rows - int(P.win_pos0[b])
+        gone = np.setdiff1d(np.arange(P.L), at)
+        P.win[b, torch.from_numpy(gone).cuda()] = float("nan")
+    P.pool.view(torch.uint8)[torch.from_numpy(~keep).cuda()] = 255
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "bf16"])
+@pytest.mark.parametrize("kw", [
+    dict(B=2, pages=40, page_rows=8, pos=[128 * 100 + 5, 128 * 3]),
+    dict(B=2, pages=6, page_rows=8, pos=[60, 128 * 21], ring=False),
+    dict(B=2, T=3, k=70, pages=20, page_rows=32, m=4, pos=[41, 2000]),
+], ids=str)
+def test_not_a_number_where_nothing_is_read(kw, fmt):
+    P = F.Problem(seed=9, fmt=fmt, **kw)
+    _poison(P)
+    if fmt == "fp4":
+        F.check_attention(P.attention(), P.out64(), str(kw))
+    got = P.mass(torch.zeros((P.B, P.N), device="cuda")).double().cpu().numpy()
+    ref = P.mass64(torch.zeros((P.B, P.N)), 1.0)
+    # an entry's weight is a sum of T * H weights, each off by a few 1e-6 of itself at most
+    assert np.abs(got - ref).max() <= 1e-5 * P.T * P.H
+
+
 @pytest.mark.parametrize("k", [0, 300])
 def test_far_offsets_and_large_logits(k):
     """Pages whose byte offset passes 2^32, and logits so large that one row takes all weight
