@@ -257,44 +257,68 @@ __global__ void __launch_bounds__(kThreads, 1) k_mass_logits(const __grid_consta
   }
 }
 
-// log2 of the softmax denominator of head h (of all H) of query bt
-__device__ __forceinline__ float denominator(const Params& P, int bt, int h) {
-  const int g = h / kHg, hh = h % kHg;
-  const float* pp = P.part + (size_t)(bt * P.G + g) * P.nsplit * (2 * kHg) + hh;
-  const float zs = P.a.sink ? P.a.sink[h] * 1.44269504088896341f : -INFINITY;
-  float M = zs;
-#pragma unroll 4
-  for (int s = 0; s < P.nsplit; ++s) M = fmaxf(M, pp[s * 2 * kHg]);
-  if (M == -INFINITY) return INFINITY;  // no row: every weight is 0
-  float t = zs == -INFINITY ? 0.f : exp2f(zs - M);
-#pragma unroll 4
-  for (int s = 0; s < P.nsplit; ++s) {
-    const float m = pp[s * 2 * kHg], l = pp[s * 2 * kHg + kHg];
-    if (m != -INFINITY) t = fmaf(l, exp2f(m - M), t);
-  }
-  return M + log2f(t);
-}
-
 constexpr int kRedThreads = 256;
 constexpr int kParts = 4;                      // threads per row, each a quarter of the heads
 constexpr int kRedRows = kRedThreads / kParts;  // 64: one tile of z
 
+// L[h] = log2 of the softmax denominator of head h of query bt, by four threads with every
+// fourth split each (one round trip, where a thread a head took two of many loads).
+__device__ __forceinline__ void denominators(const Params& P, int bt, float* L) {
+  const int q = threadIdx.x & 3;
+#pragma unroll 2
+  for (int h = threadIdx.x >> 2; h < P.a.H; h += kRedThreads / 4) {  // H: a multiple of 64
+    const float* pp = P.part + (size_t)(bt * P.G + h / kHg) * P.nsplit * (2 * kHg) + h % kHg;
+    const float zs = P.a.sink ? P.a.sink[h] * 1.44269504088896341f : -INFINITY;
+    float m[kMaxSplit / 4], l[kMaxSplit / 4], M = zs;
+#pragma unroll
+    for (int i = 0; i < kMaxSplit / 4; ++i) {
+      m[i] = -INFINITY;
+      if (q + 4 * i < P.nsplit) {
+        m[i] = pp[(q + 4 * i) * 2 * kHg];
+        l[i] = pp[(q + 4 * i) * 2 * kHg + kHg];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kMaxSplit / 4; ++i) M = fmaxf(M, m[i]);
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 1));
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 2));
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMaxSplit / 4; ++i)
+      if (m[i] != -INFINITY) t = fmaf(l[i], exp2f(m[i] - M), t);
+    t += __shfl_xor_sync(0xffffffffu, t, 1);
+    t += __shfl_xor_sync(0xffffffffu, t, 2);
+    if (zs != -INFINITY) t += exp2f(zs - M);
+    if (q == 0) L[h] = M == -INFINITY ? INFINITY : M + log2f(t);  // no row: every weight is 0
+  }
+}
+
 // The sum over all heads of 2^(z - L) for row `row` of query bt, by four threads with a
 // quarter of each group's heads each; all four get it (summed in a fixed order). L and `part`
-// are shared arrays of H and kRedThreads floats; the whole block calls.
-__device__ __forceinline__ float weight_of(const Params& P, int bt, int64_t row, bool in,
-                                           const float* L, float* part) {
-  const int p = threadIdx.x / kRedRows, r = threadIdx.x % kRedRows;
+// are shared arrays of H and kRedThreads floats; the whole block calls. The first group's z are
+// requested before L is worked out.
+__device__ __forceinline__ float weight_of(const Params& P, int bt, int64_t row, bool in, float* L,
+                                           float* part) {
+  constexpr int kMine = kHg / kParts;
+  const int p = threadIdx.x / kRedRows, r = threadIdx.x % kRedRows, c = (int)(row % kRows);
+  float zv[kMine];
+  auto load = [&](int g) {
+    const float* z = P.z + ((size_t)(bt * P.G + g) * P.z_tiles + row / kRows) * kTile;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int h = p * kMine + i;
+      zv[i] = z[h * kRows + (((c >> 3) ^ (h & 7)) << 3) + (c & 7)];
+    }
+  };
+  if (in) load(0);
+  denominators(P, bt, L);
+  __syncthreads();
   float s = 0.f;
   if (in) {
     for (int g = 0; g < P.G; ++g) {
-      const float* z = P.z + ((size_t)(bt * P.G + g) * P.z_tiles + row / kRows) * kTile;
-      const int c = (int)(row % kRows);
-#pragma unroll 16
-      for (int i = 0; i < kHg / kParts; ++i) {
-        const int h = p * (kHg / kParts) + i;
-        s += ex2(z[h * kRows + (((c >> 3) ^ (h & 7)) << 3) + (c & 7)] - L[g * kHg + h]);
-      }
+      if (g > 0) load(g);
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) s += ex2(zv[i] - L[g * kHg + p * kMine + i]);
     }
   }
   part[threadIdx.x] = s;
@@ -317,8 +341,6 @@ __global__ void __launch_bounds__(kRedThreads) k_mass_dense(const __grid_constan
     const int bt = b * P.a.T + t;
     const int64_t n_vis = make_list(P.a, P.a.q_pos[bt]).n_vis;
     if (e0 >= n_vis) continue;  // the same for the whole block
-    for (int h = threadIdx.x; h < P.a.H; h += kRedThreads) L[h] = denominator(P, bt, h);
-    __syncthreads();
     sum += weight_of(P, bt, e, e < n_vis, L, part);  // ends with a barrier: L may be rewritten
   }
   if (writer) P.acc[(size_t)b * P.a.n_cap + e] = fmaf(P.decay, old, sum);
@@ -331,8 +353,6 @@ __global__ void __launch_bounds__(kRedThreads) k_mass_sparse(const __grid_consta
   const int j = blockIdx.x * kRedRows + threadIdx.x % kRedRows;
   const int e = j < P.a.k ? P.a.idx[(size_t)bt * P.a.k + j] : -1;
   pdl_wait();
-  for (int h = threadIdx.x; h < P.a.H; h += kRedThreads) L[h] = denominator(P, bt, h);
-  __syncthreads();
   const bool in = e >= 0 && e < P.a.n_cap;
   const float w = weight_of(P, bt, j, in, L, part);
   if (!in || threadIdx.x >= kRedRows) return;
