@@ -22,6 +22,13 @@
 // The KV tile is single-buffered, but each pair of 64-value atoms is given back as soon as its
 // products are done, so the gather warps refill the first while the others are multiplied. A
 // chunk's logits leave as one bulk copy of 16 KB from a staged tile.
+//
+// What bounds it: as the attention, operands from shared memory (6 KB and 48 cycles for each 16
+// of K), then the logits, 4 bytes per (query, head, row) written and read once more (34 MB each
+// way for 16 queries x 64 heads over 8192 entries: mostly L2). Measured, whole call: that case
+// 46.1 us, 3 queries over 600 bf16 entries 10.1 us, 4 x 4 queries x 128 heads with lists of 1024
+// 25.4 us. Keeping the logits beats a second product over the rows once the maxima are known,
+// which would cost another 28 us in the first case where they cost 10.
 #include <cmath>
 
 #include "common.cuh"
