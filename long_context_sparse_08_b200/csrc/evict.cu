@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_evict_select(EvictArgs a, uint3
   extern __shared__ uint32_t smem_keys[];
   __shared__ uint32_t hist[kBins];
   __shared__ uint32_t red[2][32];
+  __shared__ uint2 votes[kThreads / 32][kPer];  // of a round: kept, present
   __shared__ int pick[3], s_last;  // digit, keys above it, keys at it
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, pr = a.page_rows;
   const int n = used_entries(a, b), used = pages_of(a, n);
@@ -117,12 +118,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_evict_select(EvictArgs a, uint3
   for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
   if (kKeys) pdl_wait();
 
-  // ---- keys: pages that are mapped, those always kept above all ----
+  // ---- keys: pages that are mapped, those always kept above all; the table goes over as it is
+  //      (evicted pages are marked below) ----
+  int32_t* nt = a.new_table + (size_t)b * a.max_pages;
   int mine = 0;
 #pragma unroll 8
   for (int k = tid; k < used; k += kThreads) {
     uint32_t key = kKeys ? wk[k] : weight_key(acc[k]);
-    if (table[k] < 0) key = 0;
+    const int32_t page = table[k];
+    nt[k] = page;
+    if (page < 0) key = 0;
     else if (k < a.keep_first || k >= used - a.keep_last) key = kAlways;
     keys[k] = key;
     mine += key != 0;
@@ -196,53 +201,48 @@ __global__ void __launch_bounds__(kThreads, 1) k_evict_select(EvictArgs a, uint3
   int32_t* out_entries = a.entries != nullptr ? a.entries + (size_t)b * n_out : nullptr;
   int32_t* out_kept = a.kept + (size_t)b * a.budget;
   int32_t* out_gone = a.evicted + (size_t)b * a.max_pages;
-  int32_t* nt = a.new_table + (size_t)b * a.max_pages;
   const uint32_t below = (1u << lane) - 1u;
   int n_kept = 0, seen = 0;
   bool last_stays = false;
   for (int k0 = 0, round = 0; k0 < used; k0 += kRound, ++round) {
     const int steps = min(kPer, (used - k0 + kThreads - 1) / kThreads);
     const int first = k0 + (tid >> 5) * (32 * steps) + lane;
-    uint32_t b_keep[kPer], b_here[kPer];
-    int32_t old[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      old[i] = i < steps && first + 32 * i < used ? table[first + 32 * i] : 0;
+    uint2* mine_of = votes[tid >> 5];
     uint32_t mine2 = 0;  // kept and present pages of the warp, 16 bits each
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const uint32_t key = i < steps && first + 32 * i < used ? keys[first + 32 * i] : 0u;
-      b_here[i] = __ballot_sync(0xffffffffu, key != 0);
-      b_keep[i] = __ballot_sync(0xffffffffu, key != 0 && (key >> shift) >= least);
-      mine2 += (uint32_t)__popc(b_keep[i]) + ((uint32_t)__popc(b_here[i]) << 16);
+#pragma unroll 2
+    for (int i = 0; i < steps; ++i) {
+      const uint32_t key = first + 32 * i < used ? keys[first + 32 * i] : 0u;
+      const uint32_t here = __ballot_sync(0xffffffffu, key != 0);
+      const uint32_t keep = __ballot_sync(0xffffffffu, key != 0 && (key >> shift) >= least);
+      if (lane == 0) mine_of[i] = make_uint2(keep, here);
+      mine2 += (uint32_t)__popc(keep) + ((uint32_t)__popc(here) << 16);
     }
     uint32_t all2;  // lane 0 speaks for its warp
     uint32_t pos = block_scan(lane == 0 ? mine2 : 0u, red[round & 1], &all2);
     pos = __shfl_sync(0xffffffffu, pos, 0);
     int kept0 = n_kept + (int)(pos & 0xffff), here0 = seen + (int)(pos >> 16);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+#pragma unroll 2
+    for (int i = 0; i < steps; ++i) {
       const int page = first + 32 * i;
-      if (i >= steps || page - lane >= used) break;
-      const bool here = (b_here[i] >> lane) & 1u, keep = (b_keep[i] >> lane) & 1u;
-      const int kept = kept0 + __popc(b_keep[i] & below);
-      if (page < used) nt[page] = here && !keep ? kEvicted : old[i];
+      const uint2 v = mine_of[i];
+      const bool here = (v.y >> lane) & 1u, keep = (v.x >> lane) & 1u;
+      const int kept = kept0 + __popc(v.x & below);
       if (keep) {
         out_kept[kept] = page;
         if (kSmem) keys[kept] = (uint32_t)page;  // every key up to here has been read
       } else if (here) {
-        out_gone[here0 + __popc(b_here[i] & below) - kept] = page;
+        nt[page] = kEvicted;
+        out_gone[here0 + __popc(v.y & below) - kept] = page;
       }
       if (page == used - 1) last_stays = keep;
-      kept0 += __popc(b_keep[i]);
-      here0 += __popc(b_here[i]);
+      kept0 += __popc(v.x);
+      here0 += __popc(v.y);
     }
     n_kept += (int)(all2 & 0xffff);
     seen += (int)(all2 >> 16);
   }
   const int n_gone = present - n_kept;
-  for (int k = used + tid; k < a.max_pages; k += kThreads)
-    a.new_table[(size_t)b * a.max_pages + k] = table[k];
+  for (int k = used + tid; k < a.max_pages; k += kThreads) nt[k] = table[k];
   for (int i = n_kept + tid; i < a.budget; i += kThreads) out_kept[i] = -1;
   for (int i = n_gone + tid; i < a.max_pages; i += kThreads) out_gone[i] = -1;
   if (tid == 0) {
