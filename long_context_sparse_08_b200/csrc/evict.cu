@@ -11,12 +11,13 @@
 //                   a page without entries, over the whole device;
 //   k_evict_select  a CTA per request: the keys in shared memory, the budget-th largest by
 //                   radix passes of 11, 11 and 10 bits (a pass that leaves nothing to decide is
-//                   the last), one scan per 8192 pages to place them, and the lists.
+//                   the last), one scan per 8192 pages to place them, and the lists;
+//   k_evict_entries (long lists of entries) writes those over the whole device.
 // 4 bytes are read per entry and a few per page, so latencies bound it. One CTA with the keys at
 // hand beat a cluster of eight per request (18 to 40 us: seven cluster barriers and sums
 // through distributed shared memory) and a CTA that read the keys from L2 in every pass (26 us).
-// Measured: 16 requests of 8192 one-entry pages 16.3 us, 4 of 8192 pages of 32 entries (lists of
-// 64000 entries written) 21.4 us, one of 600 pages 6.7 us.
+// Measured: 16 requests of 8192 one-entry pages 13.1 us, 4 of 8192 pages of 32 entries (lists of
+// 64000 entries written) 18.0 us, one of 600 pages 5.5 us.
 #include "common.cuh"
 #include "host_util.cuh"
 #include "internal.h"
@@ -100,6 +101,35 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* red, uint32
   return s - v + (wid > 0 ? before : 0);
 }
 
+// Entries [first, end) of a list: those of the kept pages page_at(0), page_at(1), .. (-1: none),
+// below n. `first` and the list are aligned to four entries.
+template <class PageAt>
+__device__ __forceinline__ void write_entries(int32_t* out, uint32_t end, uint32_t pr, int n,
+                                              uint32_t thread, uint32_t threads, PageAt page_at,
+                                              uint32_t first = 0) {
+  const bool pow2 = (pr & (pr - 1)) == 0;
+  const int log2 = 31 - __clz(pr);
+  auto div = [&](uint32_t i) { return pow2 ? i >> log2 : i / pr; };
+  if (pr % 4 == 0) {  // four entries of a page a thread (the list is then 16-byte aligned)
+#pragma unroll 1
+    for (uint32_t i = first + 4 * thread; i < end; i += 4 * threads) {
+      const uint32_t q = div(i);
+      const int page = page_at(q), e = page * (int)pr + (int)(i - q * pr);
+      int4 v = make_int4(e, e + 1, e + 2, e + 3);
+      if (page < 0) v = make_int4(-1, -1, -1, -1);
+      else if (e + 3 >= n) v = make_int4(e < n ? e : -1, e + 1 < n ? e + 1 : -1, e + 2 < n ? e + 2 : -1, -1);
+      *reinterpret_cast<int4*>(out + i) = v;
+    }
+  } else {
+#pragma unroll 1
+    for (uint32_t i = first + thread; i < end; i += threads) {
+      const uint32_t q = div(i);
+      const int page = page_at(q), e = page * (int)pr + (int)(i - q * pr);
+      out[i] = page >= 0 && e < n ? e : -1;
+    }
+  }
+}
+
 // kKeys: the keys come from k_evict_keys (in `ws`), else from acc (pages of one entry). kSmem:
 // they fit shared memory, else `ws` holds them throughout.
 template <bool kKeys, bool kSmem>
@@ -117,12 +147,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_evict_select(EvictArgs a, uint3
   const float* acc = a.acc + (size_t)b * a.max_pages * pr;
   for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
   if (kKeys) pdl_wait();
+  pdl_trigger();
 
   // ---- keys: pages that are mapped, those always kept above all; the table goes over as it is
   //      (evicted pages are marked below) ----
   int32_t* nt = a.new_table + (size_t)b * a.max_pages;
   int mine = 0;
-#pragma unroll 8
+  // (unrolled by two here and rolled below: every line of code is fetched cold, and eight-fold
+  // unrolling took 1.2 us more)
+#pragma unroll 2
   for (int k = tid; k < used; k += kThreads) {
     uint32_t key = kKeys ? wk[k] : weight_key(acc[k]);
     const int32_t page = table[k];
@@ -154,7 +187,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_evict_select(EvictArgs a, uint3
         if (!__any_sync(0xffffffffu, in)) continue;
         const uint32_t digit = in ? (key >> shift) & ((1u << bits) - 1u) : kBins;
         // equal weights: one addition for the warp (32 to one bin would go one after another)
-        if (__all_sync(0xffffffffu, digit == __shfl_sync(0xffffffffu, digit, 0))) {
+        int same;
+        __match_all_sync(0xffffffffu, digit, &same);
+        if (same) {
           if (lane == 0) atomicAdd(&hist[digit], 32u);
         } else if (in) {
           atomicAdd(&hist[digit], 1u);
@@ -259,28 +294,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_evict_select(EvictArgs a, uint3
   if (tid == 0 && !s_last) a.counts[3 * b + 1] = n_kept * pr;
   if (out_entries != nullptr) {
     __syncthreads();  // the kept pages, written by this CTA
-    const bool pow2 = (pr & (pr - 1)) == 0;
-    const int log2 = 31 - __clz(pr);
-    auto page_at = [&](uint32_t q) { return (int)q < n_kept ? (kSmem ? (int)keys[q] : out_kept[q]) : -1; };
-    auto div = [&](uint32_t i) { return pow2 ? i >> log2 : i / (uint32_t)pr; };
-    if (pr % 4 == 0) {  // four entries of a page a thread (the list is then 16-byte aligned)
-#pragma unroll 4
-      for (uint32_t i = 4 * tid; i < (uint32_t)n_out; i += 4 * kThreads) {
-        const uint32_t q = div(i);
-        const int page = page_at(q), e = page * pr + (int)(i - q * (uint32_t)pr);
-        *reinterpret_cast<int4*>(out_entries + i) =
-            make_int4(page >= 0 && e < n ? e : -1, page >= 0 && e + 1 < n ? e + 1 : -1,
-                      page >= 0 && e + 2 < n ? e + 2 : -1, page >= 0 && e + 3 < n ? e + 3 : -1);
-      }
-    } else {
-#pragma unroll 4
-      for (uint32_t i = tid; i < (uint32_t)n_out; i += kThreads) {
-        const uint32_t q = div(i);
-        const int page = page_at(q), e = page * pr + (int)(i - q * (uint32_t)pr);
-        out_entries[i] = page >= 0 && e < n ? e : -1;
-      }
-    }
+    write_entries(out_entries, (uint32_t)n_out, (uint32_t)pr, n, (uint32_t)tid, kThreads,
+                  [&](uint32_t q) { return (int)q < n_kept ? (kSmem ? (int)keys[q] : out_kept[q]) : -1; });
   }
+}
+
+// The same for long lists: one SM stores 64 bytes a cycle, so that 4 requests' lists of 64000
+// entries took 4.6 us of 19.7 in the CTAs above, and 18.0 in all with this launch. A list of 16384
+// takes one SM as long as the launch does.
+constexpr int64_t kLongList = 16384;
+constexpr int kListBlock = 4096;  // entries of a block
+
+__global__ void __launch_bounds__(256) k_evict_entries(EvictArgs a) {
+  const int b = blockIdx.y;
+  const int64_t n_out = (int64_t)a.budget * a.page_rows;
+  const int n = used_entries(a, b);
+  const int32_t* kept = a.kept + (size_t)b * a.budget;
+  pdl_wait();
+  const int n_kept = a.counts[3 * b];
+  const int64_t first = (int64_t)blockIdx.x * kListBlock;
+  write_entries(a.entries + (size_t)b * n_out,
+                (uint32_t)(n_out - first < kListBlock ? n_out : first + kListBlock), (uint32_t)a.page_rows, n, (uint32_t)threadIdx.x, 256,
+                [&](uint32_t q) { return (int)q < n_kept ? kept[q] : -1; }, (uint32_t)first);
 }
 
 }  // namespace
@@ -310,7 +345,13 @@ cudaError_t launch_evict(const EvictArgs& a, void* ws, cudaStream_t st) {
   static std::atomic<uint64_t> allowed[4];
   e = allow_smem(kern, kSmemKeys * (int)sizeof(uint32_t), allowed[2 * own + fits]);
   if (e != cudaSuccess) return e;
-  return launch(own, kern, dim3((unsigned)a.B), dim3(kThreads), smem, st, a, keys);
+  const int64_t n_out = a.entries != nullptr ? (int64_t)a.budget * a.page_rows : 0;
+  EvictArgs sel = a;
+  if (n_out > kLongList) sel.entries = nullptr;
+  e = launch(own, kern, dim3((unsigned)a.B), dim3(kThreads), smem, st, sel, keys);
+  if (e != cudaSuccess || n_out <= kLongList) return e;
+  const dim3 grid((unsigned)((n_out + kListBlock - 1) / kListBlock), (unsigned)a.B);
+  return launch(true, k_evict_entries, grid, dim3(256), 0, st, a);
 }
 
 }  // namespace csa
