@@ -84,7 +84,7 @@ struct Smem {
   uint64_t item_full[kItems];
   uint64_t kv_full[kBuf], kv_free[kBuf * kFree], s_full[kBuf], p_full[kBuf], q_full, done[2];
   uint32_t tmem_slot;
-  float alpha[kHg], fin[kHg];
+  alignas(16) float alpha[kHg], fin[kHg];
 };
 
 struct Params {
@@ -447,14 +447,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
       }
       // ---- epilogue ----
       pdl_wait();  // the rotation, written beside the tiles
-      // dims d = r, r + 8 of 32 warp + 16 half (r = lane / 4) of the last slice's last two warps
-      float2 rot[2][2];
-      if (warp >= 2) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          rot[i >> 1][i & 1] =
-              P.rope[(size_t)x.bt * 32 + ((32 * (warp - 2) + 8 * i + (lane >> 2)) >> 1)];
-      }
+      // rotation of dim 32 (warp - 2) + lane of the last half slice
+      const float2 rot = warp >= 2 ? P.rope[(size_t)x.bt * 32 + 16 * (warp - 2) + (lane >> 1)]
+                                   : make_float2(1.f, 0.f);
       const int h0 = (x.stream - x.bt * P.G) * kHg;
       const bool single = P.nsplit == 1;
       float* pp = P.part + (size_t)x.w * kPartFloats;
@@ -482,71 +477,45 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
       bar_softmax();  // S.fin
       tc_fence_after();
       if (single) {
-        // Per slice of 128 dims, each warp its 32 (two pieces of 16 lanes): pairs of heads become
-        // bf16x2, stored transposed into [head][32 dims] in the warp's quarter of the P buffers
-        // (idle until the next item's first P), then 64 bytes of every head's row go out. The
-        // 16-byte pieces are permuted by head / 2, so that eight heads' fall into distinct banks.
-        const uint32_t st = smem_u32(base + kOffP) + warp * (kHg * 64);
-        float f0[8], f1[8];  // of heads 8 i + 2 quad, + 1
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          f0[i] = S.fin[8 * i + 2 * quad];
-          f1[i] = S.fin[8 * i + 2 * quad + 1];
-        }
-        const int oh = lane >> 2, oc = lane & 3;  // head of eight and 16-byte piece written out
-        const uint8_t* from = base + kOffP + warp * (kHg * 64) + oh * 64 + ((oc ^ (oh >> 1)) << 4);
+        // A lane has a dim of every slice, for all heads. Neighbouring lanes trade values, so that
+        // the even one has dims d, d + 1 of head h and the odd one those of head h + 1: 64 bytes of
+        // a head's row per half warp, straight from registers (through shared memory, in 16-byte
+        // pieces, an item took 2500 cycles more).
+        const bool odd = lane & 1;
         uint8_t* out = reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(a.out) +
-                                                  ((size_t)x.bt * a.H + h0) * kC) +
-                       oh * (kC * 2) + 64 * warp + 16 * oc;
+                                                  ((size_t)x.bt * a.H + h0 + odd) * kC + 32 * warp +
+                                                  (lane & ~1));
 #pragma unroll 1
         for (int sl = 0; sl < 4; ++sl, out += 256) {
-          uint32_t o[2][32];
+          uint32_t o[64];
           if (have) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-              tmem_ld_16x256b_x8(lane_base + ((uint32_t)(16 * half) << 16) + kColO + 64 * sl, o[half]);
+            tmem_ld_32x32b_x64(lane_base + kColO + 64 * sl, o);
             tmem_ld_wait();
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[0][i] = o[1][i] = 0u;
+            for (int h = 0; h < kHg; ++h) o[h] = 0u;
+          }
+          float* y = reinterpret_cast<float*>(o);
+#pragma unroll
+          for (int h = 0; h < kHg; h += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(S.fin + h);
+            y[h] *= f.x;
+            y[h + 1] *= f.y;
+            y[h + 2] *= f.z;
+            y[h + 3] *= f.w;
+          }
+          if (sl == 3 && warp >= 2) {  // by -t: (u, v) turns to (u c + v s, v c - u s)
+            const float sn = odd ? -rot.y : rot.y;
+#pragma unroll
+            for (int h = 0; h < kHg; ++h)
+              y[h] = y[h] * rot.x + __shfl_xor_sync(0xffffffffu, y[h], 1) * sn;
           }
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            // registers 4 i, + 1: heads 8 i + 2 quad, + 1 of dim r = lane / 4; + 2, + 3: of dim r + 8
-            float y[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              y[i] = __uint_as_float(o[half][i]) * ((i & 1) ? f1[i >> 2] : f0[i >> 2]);
-            if (128 * sl + 32 * warp >= kNope) {  // rotation by -t: dims d, d ^ 1 are lanes l, l ^ 4
-              const float sg = (lane & 4) ? -1.f : 1.f;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float other = __shfl_xor_sync(0xffffffffu, y[i], 4);
-                const float2 c = rot[half][(i >> 1) & 1];
-                y[i] = y[i] * c.x + sg * other * c.y;
-              }
-            }
-            // pieces of 8 dims x 8 heads; the transposed store writes, for head row r of a piece,
-            // its 8 dims: piece 2 i + (dims + 8); 16-byte piece 2 half + dims + 8 of the 64 bytes
-            const int chunk = 2 * half + ((lane >> 3) & 1), r = lane & 7;
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              uint32_t p[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int e = 4 * (i + (k >> 1)) + 2 * (k & 1);
-                p[k] = pack2<kBf16>(y[e], y[e + 1]);
-              }
-              stmatrix_x4_trans(st + (8 * (i + (lane >> 4)) + r) * 64 + ((chunk ^ (r >> 1)) << 4), p[0],
-                                p[1], p[2], p[3]);
-            }
+          for (int h = 0; h < kHg; h += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? y[h] : y[h + 1], 1);
+            *reinterpret_cast<uint32_t*>(out + h * (kC * 2)) =
+                odd ? pack2<kBf16>(got, y[h + 1]) : pack2<kBf16>(y[h], got);
           }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4*>(out + (size_t)i * (8 * kC * 2)) =
-                *reinterpret_cast<const uint4*>(from + i * (8 * 64));
-          __syncwarp();
         }
         tc_fence_before();
       } else {
