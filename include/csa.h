@@ -374,8 +374,8 @@ csa_status csa_index_topk_paged(const csa_params* p, int32_t B, int32_t T,
  * updated in place (every entry decays; an entry listed twice gets both weights). kv->fmt is
  * CSA_BF16 or CSA_MIXED_MXFP4_BF16, else CSA_ERR_UNSUPPORTED. Logits, sums and weights are fp32
  * (q_hat enters the products as two 16-bit parts); the same inputs give the same bits. decay in
- * [0, 1]. c = 512, rope_dims = 64, n_heads a multiple of 64, B * T <= 65535 and T * n_heads <=
- * 2^22. With B * T = 0 acc is left as it is. Pages and evicted pages as in the attention (device
+ * [0, 1]. c = 512, rope_dims = 64, n_heads a multiple of 64 and at most 8192, B * T <= 65535 and
+ * T * n_heads <= 2^22. With B * T = 0 acc is left as it is. Pages and evicted pages as in the attention (device
  * error code 226). Workspace: csa_attn_mass_workspace_size (sparse = 1 with an index list):
  * 4 bytes per (query, head, row).
  */

@@ -974,6 +974,7 @@ csa_status check_mass(const csa_params* p, int32_t B, int32_t T, int64_t N_cap, 
   TRY(check_sizes(B, T, N_cap));
   if (sparse) TRY(check_topk(p));
   REQUIRE((int64_t)B * T <= 65535, "the attention weight takes at most 65535 queries per call");
+  REQUIRE(p->n_heads <= 8192, "the attention weight takes at most 8192 heads");
   REQUIRE((int64_t)T * p->n_heads <= (1 << 22), "T * n_heads too large");
   auto a = make_mqa(p, B, T, nullptr, nullptr, nullptr, N_cap, nullptr, sparse ? p->topk : 0,
                     nullptr, 0, nullptr, nullptr, nullptr, nullptr);

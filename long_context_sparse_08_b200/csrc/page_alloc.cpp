@@ -103,10 +103,14 @@ csa_status csa_page_alloc_evict(csa_page_alloc* a, int32_t b, const int32_t* pag
       return csa::report_error(CSA_ERR_INVALID_ARG,
                                "logical page %d of request %d is not mapped, or the list is not "
                                "ascending", pages[i], b);
-  for (int32_t i = 0; i < n; ++i) {
-    a->free_list.push_back(row[pages[i]]);
-    row[pages[i]] = csa::kEvicted;
+  int32_t given = 0;
+  try {
+    for (; given < n; ++given) a->free_list.push_back(row[pages[given]]);
+  } catch (const std::bad_alloc&) {
+    while (given-- > 0) a->free_list.pop_back();
+    return csa::report_error(CSA_ERR_INVALID_ARG, "host allocation failed");
   }
+  for (int32_t i = 0; i < n; ++i) row[pages[i]] = csa::kEvicted;
   return csa::report_error(CSA_OK, "");
 }
 

@@ -112,6 +112,7 @@ def test_attention_weight():
     assert call(B_=65535, T=2, pos0=FAKE) == INVALID
     wide = csa.make_params(m=128, overlap=0, n_heads=128)
     assert call(params=wide, T=32769, B_=1, pos0=FAKE) == INVALID  # T * n_heads > 2^22
+    assert call(params=csa.make_params(m=128, overlap=0, n_heads=8256)) == INVALID
     assert call(kv=fp4(fmt=csa.CSA_MIXED_FP8_BF16, scales=FAKE)) == UNSUPPORTED
     assert call(kv=fp4(fmt=csa.CSA_MXFP4)) == INVALID
     for bad in (dict(rope_dims=32), dict(n_heads=16), dict(c=256)):
