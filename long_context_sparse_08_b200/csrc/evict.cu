@@ -16,8 +16,8 @@
 // 4 bytes are read per entry and a few per page, so latencies bound it. One CTA with the keys at
 // hand beat a cluster of eight per request (18 to 40 us: seven cluster barriers and sums
 // through distributed shared memory) and a CTA that read the keys from L2 in every pass (26 us).
-// Measured: 16 requests of 8192 one-entry pages 13.1 us, 4 of 8192 pages of 32 entries (lists of
-// 64000 entries written) 18.0 us, one of 600 pages 5.5 us.
+// Measured: 16 requests of 8192 one-entry pages 12.8 us, 4 of 8192 pages of 32 entries (lists of
+// 64000 entries written) 17.6 us, one of 600 pages 5.3 us.
 #include "common.cuh"
 #include "host_util.cuh"
 #include "internal.h"
@@ -54,8 +54,10 @@ __global__ void __launch_bounds__(256) k_evict_keys(EvictArgs a, uint32_t* keys,
   const int b = blockIdx.y;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t p64 = i / lanes;
-  const int n = used_entries(a, b), sub = (int)(i % lanes);
+  const int sub = (int)(i % lanes);
+  pdl_wait();
   pdl_trigger();
+  const int n = used_entries(a, b);
   const int page = p64 < a.max_pages ? (int)p64 : a.max_pages;  // whole warps stay for the exchange
   uint32_t key = 0;
   if (page < a.max_pages) {
@@ -140,12 +142,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_evict_select(EvictArgs a, uint3
   __shared__ uint2 votes[kThreads / 32][kPer];  // of a round: kept, present
   __shared__ int pick[3], s_last;  // digit, keys above it, keys at it
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, pr = a.page_rows;
+  for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
+  if (!kKeys) pdl_wait();  // (with keys, the kernel that made them has waited)
   const int n = used_entries(a, b), used = pages_of(a, n);
   uint32_t* wk = ws + (size_t)b * a.max_pages;
   uint32_t* keys = kSmem ? smem_keys : wk;
   const int32_t* table = a.page_table + (size_t)b * a.max_pages;
   const float* acc = a.acc + (size_t)b * a.max_pages * pr;
-  for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
   if (kKeys) pdl_wait();
   pdl_trigger();
 
@@ -335,7 +338,7 @@ cudaError_t launch_evict(const EvictArgs& a, void* ws, cudaStream_t st) {
     while (lanes < 32 && 2 * lanes <= units) lanes *= 2;
     const int64_t threads = (int64_t)a.max_pages * lanes;
     const dim3 grid((unsigned)((threads + 255) / 256), (unsigned)a.B);
-    e = launch(false, vec ? k_evict_keys<true> : k_evict_keys<false>, grid, dim3(256), 0, st, a, keys,
+    e = launch(true, vec ? k_evict_keys<true> : k_evict_keys<false>, grid, dim3(256), 0, st, a, keys,
                lanes);
     if (e != cudaSuccess) return e;
   }
@@ -348,7 +351,7 @@ cudaError_t launch_evict(const EvictArgs& a, void* ws, cudaStream_t st) {
   const int64_t n_out = a.entries != nullptr ? (int64_t)a.budget * a.page_rows : 0;
   EvictArgs sel = a;
   if (n_out > kLongList) sel.entries = nullptr;
-  e = launch(own, kern, dim3((unsigned)a.B), dim3(kThreads), smem, st, sel, keys);
+  e = launch(true, kern, dim3((unsigned)a.B), dim3(kThreads), smem, st, sel, keys);
   if (e != cudaSuccess || n_out <= kLongList) return e;
   const dim3 grid((unsigned)((n_out + kListBlock - 1) / kListBlock), (unsigned)a.B);
   return launch(true, k_evict_entries, grid, dim3(256), 0, st, a);
