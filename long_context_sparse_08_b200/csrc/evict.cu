@@ -223,9 +223,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_evict_select(EvictArgs a, uint3
       int before = 0;
       for (int k0 = 0, round = 0; k0 < used; k0 += kThreads, ++round) {
         const bool tie = k0 + tid < used && keys[k0 + tid] == tau;
-        const uint32_t votes = __ballot_sync(0xffffffffu, tie);
-        uint32_t at = block_scan(lane == 0 ? (uint32_t)__popc(votes) : 0u, red[round & 1], &total);
-        at = __shfl_sync(0xffffffffu, at, 0) + __popc(votes & ((1u << lane) - 1u));
+        const uint32_t ties = __ballot_sync(0xffffffffu, tie);
+        uint32_t at = block_scan(lane == 0 ? (uint32_t)__popc(ties) : 0u, red[round & 1], &total);
+        at = __shfl_sync(0xffffffffu, at, 0) + __popc(ties & ((1u << lane) - 1u));
         if (tie && before + (int)at < want) keys[k0 + tid] = kAlways;
         before += (int)total;
       }

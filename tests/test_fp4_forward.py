@@ -122,3 +122,66 @@ def test_two_streams_at_once():
             table = P.table[b].copy()
             table[gone] = -2
             assert r["table"][b].tolist() == table.tolist()  # written over its own input
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_one_after_another_on_one_workspace(captured):
+    """Attention of few and of many queries, weight and eviction in turn, each with inputs that a
+    copy just before it wrote, all on one workspace and with nothing waited for in between."""
+    few = F.Problem(B=2, pages=70, page_rows=8, seed=31)
+    many = F.Problem(B=3, T=70, k=40, pages=20, page_rows=32, m=4, pos=[2000, 900, 41], seed=32)
+    need = max([csa.workspace_size(few.p, csa.CSA_WS_HCA_MQA, few.kv_fmt, 2, 1, few.N),
+                csa.workspace_size(many.p, csa.CSA_WS_SPARSE_MQA, many.kv_fmt, 3, 70, many.N),
+                csa.attn_mass_workspace_size(few.p, 2, 1, few.N, 0),
+                csa.evict_pages_workspace_size(2, few.pages)])
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    n = 6
+    q_few = [torch.roll(few.q, i, 3).contiguous() for i in range(n)]
+    q_many = [torch.roll(many.q, i, 3).contiguous() for i in range(n)]
+    pos = torch.from_numpy(few.pos[:, 0] - 1).cuda()
+    budget = 20
+
+    def buffers():
+        return dict(few=[torch.zeros_like(few.q) for _ in range(n)],
+                    many=[torch.zeros_like(many.q) for _ in range(n)],
+                    acc=[torch.zeros((2, few.N), device="cuda") for _ in range(n)],
+                    kept=[torch.zeros((2, budget), dtype=torch.int32, device="cuda") for _ in range(n)])
+
+    table = torch.empty_like(few.table_d)
+    gone = torch.empty_like(few.table_d)
+    counts = torch.empty((2, 3), dtype=torch.int32, device="cuda")
+
+    def steps(b, wait):
+        for i in range(n):
+            few.q.copy_(q_few[i])
+            wait()
+            few.attention(out=b["few"][i], ws=ws)
+            wait()
+            few.mass(b["acc"][i], 0.5, ws=ws)
+            wait()
+            csa.csa_evict_pages(few.p, 2, few.page_rows, few.pages, pos, b["acc"][i], few.table_d,
+                                budget, 1, 1, table, b["kept"][i], None, gone, counts, ws, need)
+            wait()
+            many.q.copy_(q_many[i])
+            many.attention(out=b["many"][i], ws=ws)
+            wait()
+            few.attention(out=b["few"][i], ws=ws)
+            wait()
+
+    want, got = buffers(), buffers()
+    steps(want, torch.cuda.synchronize)
+    if captured:
+        s = torch.cuda.Stream()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            steps(got, lambda: None)
+        for _ in range(3):
+            for acc in got["acc"]:
+                acc.zero_()
+            g.replay()
+    else:
+        steps(got, lambda: None)
+    torch.cuda.synchronize()
+    for key in want:
+        for i in range(n):
+            assert torch.equal(want[key][i], got[key][i]), (key, i)
