@@ -142,6 +142,19 @@ def test_far_offsets_and_large_logits(k):
     F.check_attention(got, P.out64(), "far", scale=1.5)
 
 
+@pytest.mark.parametrize("kw", [
+    dict(B=80, H=128, pages=20, page_rows=16),               # a stream a CTA, seven chunks
+    dict(B=3, T=60, k=500, pages=30, page_rows=32, m=4),     # several streams a CTA
+    dict(B=16, pages=400, page_rows=8),                      # nine splits of several chunks
+    dict(B=16, pages=400, page_rows=8, sink=False, n_win=0),
+], ids=str)
+def test_maxima_raised_in_later_chunks(kw):
+    """Logits with a standard deviation of 34: most chunks raise some head's running maximum by
+    more than any threshold would let pass."""
+    P = F.Problem(seed=8, scale=1.5, **kw)
+    F.check_attention(P.attention(), P.out64(), str(kw), scale=1.5)
+
+
 def test_graph_replay_other_stream_and_repeatability():
     P = F.Problem(B=2, pages=70, page_rows=8, seed=7, H=128)
     ref = P.attention()
