@@ -138,7 +138,9 @@ template <bool kKeys, bool kSmem>
 __global__ void __launch_bounds__(kThreads, 1) k_evict_select(EvictArgs a, uint32_t* ws) {
   extern __shared__ uint32_t smem_keys[];
   __shared__ uint32_t hist[kBins];
-  __shared__ uint32_t red[2][32];
+  // block_scan's sums: two arrays in turn, and one of the first scan's own: a request within its
+  // budget goes from that scan straight to the placement's, with no barrier between
+  __shared__ uint32_t red[3][32];
   __shared__ uint2 votes[kThreads / 32][kPer];  // of a round: kept, present
   __shared__ int pick[3], s_last;  // digit, keys above it, keys at it
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, pr = a.page_rows;
@@ -169,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_evict_select(EvictArgs a, uint3
     mine += key != 0;
   }
   uint32_t total;
-  block_scan((uint32_t)mine, red[0], &total);  // (its barrier also publishes keys and bins)
+  block_scan((uint32_t)mine, red[2], &total);  // (its barrier also publishes keys and bins)
   const int present = (int)total;
 
   // ---- which stay: those with key >> shift >= least, the budget-th largest key or its decided
