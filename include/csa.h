@@ -371,7 +371,8 @@ csa_status csa_index_topk_paged(const csa_params* p, int32_t B, int32_t T,
  * hca_dense_mqa_paged (idx NULL: every visible entry), window and sink in the denominator. It is
  * what csa_evict_pages chooses by: call it beside the attention, on every decode step or every
  * few, or on the last queries of a prefill. acc: fp32 [B, N_cap], N_cap = page_rows * max_pages,
- * updated in place (every entry decays; an entry listed twice gets both weights). kv->fmt is
+ * updated in place (every entry decays; an entry listed twice gets both weights; where one of a
+ * query's rows is NaN, all its weights are). kv->fmt is
  * CSA_BF16 or CSA_MIXED_MXFP4_BF16, else CSA_ERR_UNSUPPORTED. Logits, sums and weights are fp32
  * (q_hat enters the products as two 16-bit parts); the same inputs give the same bits. decay in
  * [0, 1]. c = 512, rope_dims = 64, n_heads a multiple of 64 and at most 8192, B * T <= 65535 and

@@ -228,14 +228,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_mass_logits(const __grid_consta
       if (tid == 0 && j < x.l.nc) bulk_store(zt + (size_t)j * kTile, stage, kTile * 4);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float mn = fmaxf(m[h], cm[h]);
-        if (mn != -INFINITY) {
-          float s2[2] = {0.f, 0.f};
+        // (fmaxf passes over a NaN, the sum does not: rows that are all NaN or masked are summed
+        // against 0)
+        const float mn = fmaxf(m[h], cm[h]), ref = mn == -INFINITY ? 0.f : mn;
+        float s2[2] = {0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < 16; ++i) s2[i & 1] += ex2(z[4 * (i >> 1) + 2 * h + (i & 1)] - mn);
-          sum[h] = sum[h] * ex2(m[h] - mn) + (s2[0] + s2[1]);
-          m[h] = mn;
-        }
+        for (int i = 0; i < 16; ++i) s2[i & 1] += ex2(z[4 * (i >> 1) + 2 * h + (i & 1)] - ref);
+        sum[h] = sum[h] * ex2(m[h] - ref) + (s2[0] + s2[1]);
+        m[h] = mn;
       }
     }
     // the four threads of a head
@@ -280,6 +280,7 @@ __device__ __forceinline__ void denominators(const Params& P, int bt, float* L) 
 #pragma unroll
     for (int i = 0; i < kMaxSplit / 4; ++i) {
       m[i] = -INFINITY;
+      l[i] = 0.f;
       if (q + 4 * i < P.nsplit) {
         m[i] = pp[(q + 4 * i) * 2 * kHg];
         l[i] = pp[(q + 4 * i) * 2 * kHg + kHg];
@@ -291,12 +292,12 @@ __device__ __forceinline__ void denominators(const Params& P, int bt, float* L) 
     M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 2));
     float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < kMaxSplit / 4; ++i)
-      if (m[i] != -INFINITY) t = fmaf(l[i], exp2f(m[i] - M), t);
+    for (int i = 0; i < kMaxSplit / 4; ++i)  // a split of no row has l = 0, one of NaN alone l = NaN
+      t = fmaf(l[i], m[i] == -INFINITY ? 0.f : exp2f(m[i] - M), t);
     t += __shfl_xor_sync(0xffffffffu, t, 1);
     t += __shfl_xor_sync(0xffffffffu, t, 2);
     if (zs != -INFINITY) t += exp2f(zs - M);
-    if (q == 0) L[h] = M == -INFINITY ? INFINITY : M + log2f(t);  // no row: every weight is 0
+    if (q == 0) L[h] = M == -INFINITY && t == 0.f ? INFINITY : M + log2f(t);  // no row: weights of 0
   }
 }
 
