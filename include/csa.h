@@ -328,8 +328,11 @@ typedef struct {
  * multiple of 64; mixed rows: rope_dims a multiple of 16 in (0, 512)), else
  * CSA_ERR_UNSUPPORTED. Workspace: csa_workspace_size() with N_cap = page_rows * max_pages.
  * 4-bit rows (fmt = CSA_MIXED_MXFP4_BF16; rope_dims = 64, else CSA_ERR_UNSUPPORTED) take the
- * workspace of kdt = CSA_MIXED_MXFP4_BF16. Their operands are f16 (window and RoPE values up to
- * 65504 in magnitude; a larger one becomes infinite), the sums fp32.
+ * workspace of kdt = CSA_MIXED_MXFP4_BF16. Their operands are f16, the sums fp32: window and RoPE
+ * values and q_hat (RMSNorm(q) q_rms_w, so at most sqrt(c) times the largest |q_rms_w|) beyond 65504
+ * in magnitude become infinite and those below 2^-14 keep an absolute step of 2^-24; q_hat is rounded
+ * to 11 bits; a row's weight in the output to 11 bits or to 2^-33.5 of the head's largest, whichever
+ * is more (so n rows of the least weight may be off by n 2^-33.5 of the output in all).
  */
 csa_status csa_sparse_mqa_paged(const csa_params* p, int32_t B, int32_t T, const void* q,
                                 const int64_t* q_pos, const csa_paged_kv* kv, const int32_t* idx,

@@ -18,8 +18,13 @@
 // O^T; 5 resolves addresses; 7-15 each widen one 64-value atom of every row (kv_rows.cuh). Two
 // KV buffers: S of chunk j + 1 may be issued before O^T of chunk j, so the tensor cores work
 // during the softmax, and the gather warps fill the buffer that O^T released.
-// The running max m_h is raised only when a chunk's max exceeds it by more than 2^11.5 (then
-// O^T and l are rescaled); P stays below 2^11.5, inside f16, and sums are fp32.
+// The exponent's reference m_h is set 8.5 below a chunk's largest logit (log2 units), and anew only
+// when a later chunk's passes it by more than 15 (then O^T and l are rescaled): a head's largest P
+// lies between 2^8.5 and 2^15, inside f16, and sums are fp32. f16 has steps of 2^-24 below 2^-14, so
+// a row's weight is off by 2^-11 of itself or 2^-33.5 of the head's largest, whichever is more: over
+// n rows by n 2^-33.5 of the output, 2^-13.5 at a million. (With P near 1 for the largest, rows below
+// 2^-25 of it would be lost from O and kept in l: 2^-8.5 of the output over 262144 rows.) Set 9.5
+// below and anew above 14.5, dense decode took 42.8 instead of 42.1 us, for more rescaling.
 // One split: the CTA finalises. Several: it writes (m, l, O) partials and k_attn_fp4_combine
 // merges them in a fixed order.
 //
@@ -53,7 +58,9 @@ using namespace rows;
 constexpr int kThreads = (7 + kGatherWarps) * 32;
 constexpr int kBuf = 2;
 constexpr int kFree = 4;  // a buffer is given back in four pairs of atoms, one per slice of O^T
-constexpr float kLazy = 11.5f;  // rescale threshold (log2 units)
+constexpr float kUp = 8.5f;     // log2 of P where the reference is set, at a chunk's maximum
+constexpr float kTop = 15.f;    // the reference is set anew above this (f16 ends at 2^16; a logit's
+                                // rounding to fp32 may add to the difference)
 constexpr int kMaxSplit = 32;
 
 constexpr int kSlotKV = kAtoms * kAtomBytes;  // 64 KB
@@ -365,9 +372,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fp4(const __grid_constant_
         for (int h = 0; h < 2; ++h) {
           cm[h] *= P.scale2;
           al[h] = 1.f;
-          if (cm[h] > mu[h] + kLazy || (mu[h] == -INFINITY && cm[h] != -INFINITY)) {
-            al[h] = mu[h] == -INFINITY ? 0.f : ex2(mu[h] - cm[h]);
-            mu[h] = cm[h];
+          if (cm[h] > mu[h] + kTop || (mu[h] == -INFINITY && cm[h] != -INFINITY)) {
+            const float to = cm[h] - kUp;
+            al[h] = mu[h] == -INFINITY ? 0.f : ex2(mu[h] - to);
+            mu[h] = to;
           }
           lsum[h] *= al[h];
           mref[h] = mu[h] == -INFINITY ? 0.f : mu[h];
