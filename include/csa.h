@@ -552,7 +552,10 @@ csa_status csa_forward(const csa_params* p, csa_dtype io, int32_t B, int32_t T,
  * Bytes of workspace the call `entry` needs for these sizes (0 if none). Returns 0 and
  * sets csa_last_error() on invalid sizes. kdt: the indexer key format (for the index and forward
  * calls); for CSA_WS_SPARSE_MQA and CSA_WS_HCA_MQA CSA_MIXED_MXFP4_BF16 sizes the attention over
- * 4-bit rows and any other value the one over bf16 / FP8 rows.
+ * 4-bit rows and any other value the one over bf16 / FP8 rows. CSA_WS_FORWARD is enough for every
+ * format of KV rows; csa_forward, and csa_forward_paged over bf16 / FP8 rows, accept less where the
+ * attention over 4-bit rows alone would take it (its other form: the sizes of CSA_WS_INDEX_TOPK and
+ * CSA_WS_SPARSE_MQA and, at c = 512 with n_heads a multiple of 64, 2 c bytes per head).
  */
 size_t csa_workspace_size(const csa_params* p, int32_t entry, csa_dtype kdt, int32_t B,
                           int32_t T, int64_t N_cap);

@@ -221,6 +221,15 @@ size_t scores_bytes(int32_t B, int32_t T, int64_t N_cap) {
   return round_up((size_t)B * T * (size_t)N_cap * sizeof(float));
 }
 
+// csa_forward and csa_forward_paged: the selection's bytes, then the attention over bf16 / FP8 rows
+// with its q_hat, or the attention over 4-bit rows
+size_t forward_bytes(const csa_params* p, int32_t B, int32_t T, int64_t N_cap, bool fp4) {
+  csa::MqaArgs m = make_mqa(p, B, T, nullptr, nullptr, nullptr, N_cap, nullptr, p->topk, nullptr,
+                            0, nullptr, nullptr, nullptr, nullptr);
+  return scores_bytes(B, T, N_cap) + round_up(csa::topk_workspace_bytes(B, T, N_cap, p->topk)) +
+         round_up(attn_bytes(m, fp4)) + (fp4 ? 0 : qhat_bytes(p, B, T, N_cap));
+}
+
 // index scores, then top-k; for few long rows the indexer also fills the top-k histogram
 csa_status index_then_topk(const csa_params* p, csa_dtype kdt, int32_t B, int32_t T,
                            int64_t N_cap, const void* qI, const void* qI_scale, const float* w,
@@ -331,9 +340,7 @@ size_t csa_workspace_size(const csa_params* p, int32_t entry, csa_dtype kdt, int
       m.k = 0;
       return round_up(attn_bytes(m, fp4));
     case CSA_WS_FORWARD:  // kdt names the keys here: room for the attention of any KV format
-      return scores_bytes(B, T, N_cap) + topk_ws +
-             std::max(round_up(attn_bytes(m, false)) + qhat_bytes(p, B, T, N_cap),
-                      round_up(attn_bytes(m, true)));
+      return std::max(forward_bytes(p, B, T, N_cap, false), forward_bytes(p, B, T, N_cap, true));
     default:
       fail(CSA_ERR_INVALID_ARG, "unknown workspace entry %d", entry);
       return 0;
@@ -1084,7 +1091,7 @@ csa_status csa_forward(const csa_params* p, csa_dtype io, int32_t B, int32_t T,
   if ((int64_t)B * T == 0) return ok();
   REQUIRE_PTR(a->out_idx);
   OPTIONAL_PTR(a->out_scores);
-  const size_t need = csa_workspace_size(p, CSA_WS_FORWARD, a->idx_dtype, B, T, a->N_cap);
+  const size_t need = forward_bytes(p, B, T, a->N_cap, false);
   if (ws == nullptr || ws_bytes < need || !aligned16(ws))
     return fail(CSA_ERR_WORKSPACE, "csa_forward needs %zu workspace bytes (got %zu)", need,
                 ws_bytes);
@@ -1164,7 +1171,7 @@ csa_status csa_forward_paged(const csa_params* p, int32_t B, int32_t T, const cs
     return fail(CSA_ERR_UNSUPPORTED,
                 "csa_forward_paged: needs the tensor-core attention (c = 512, n_heads a multiple "
                 "of 64; mixed rows: rope_dims a multiple of 16 in (0, 512))");
-  const size_t need = csa_workspace_size(p, CSA_WS_FORWARD, keys->fmt, B, T, N_cap);
+  const size_t need = forward_bytes(p, B, T, N_cap, lay.fp4);
   if (ws == nullptr || ws_bytes < need || !aligned16(ws))
     return fail(CSA_ERR_WORKSPACE, "csa_forward_paged needs %zu workspace bytes (got %zu)", need,
                 ws_bytes);
