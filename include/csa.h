@@ -376,8 +376,11 @@ csa_status csa_index_topk_paged(const csa_params* p, int32_t B, int32_t T,
  * few, or on the last queries of a prefill. acc: fp32 [B, N_cap], N_cap = page_rows * max_pages,
  * updated in place (every entry decays; an entry listed twice gets both weights; where one of a
  * query's rows is NaN, all its weights are). kv->fmt is
- * CSA_BF16 or CSA_MIXED_MXFP4_BF16, else CSA_ERR_UNSUPPORTED. Logits, sums and weights are fp32
- * (q_hat enters the products as two 16-bit parts); the same inputs give the same bits. decay in
+ * CSA_BF16 or CSA_MIXED_MXFP4_BF16, else CSA_ERR_UNSUPPORTED. Logits, weights and a query's sums are
+ * fp32 (q_hat enters the products as two 16-bit parts: 16 bits of it over bf16 rows; 22 bits over
+ * 4-bit rows, with f16's range as in the attention); an entry's sum over a call's lists is exact in
+ * steps of 2^-62 of T * n_heads rounded up to a power of two (2^-56 for one query of 64 heads). The
+ * same inputs give the same bits. decay in
  * [0, 1]. c = 512, rope_dims = 64, n_heads a multiple of 64 and at most 8192, B * T <= 65535 and
  * T * n_heads <= 2^22. With B * T = 0 acc is left as it is. Pages and evicted pages as in the attention (device
  * error code 226). Workspace: csa_attn_mass_workspace_size (sparse = 1 with an index list):

@@ -16,8 +16,11 @@
 //   k_mass_logits   (a CTA per (query, 64 heads, split)) writes z as fp32 and, per split and
 //                   head, the running maximum and sum;
 //   k_mass_dense    adds 2^(z - L) over queries and heads, four threads to an entry;
-//   k_mass_sparse   does so for a list slot and adds the result to a 64-bit fixed-point array
-//                   (2^-40), whose order of additions changes nothing;
+//   k_mass_sparse   does so for a list slot and adds the result to a 64-bit fixed-point array,
+//                   whose order of additions changes nothing. An entry's sum is T * H at most (a
+//                   query's rows share a weight of 1 per head), so its steps are 2^-62 of that,
+//                   rounded up to a power of two: 2^-56 for a query of 64 heads, 2^-40 at the
+//                   largest T * H (2^22) that a call takes;
 //   k_mass_finish   acc = decay * acc + that array.
 // The KV tile is single-buffered, but each pair of 64-value atoms is given back as soon as its
 // products are done, so the gather warps refill the first while the others are multiplied. A
@@ -55,8 +58,7 @@ constexpr int kTile = kHg * kRows;
 constexpr int kOffEnd = kOffZ + kTile * 4;
 constexpr int kPairs = kAtoms / 2;                // pairs of atoms, given back one by one
 constexpr uint32_t kTmemCols = 128;               // two S tiles of 64 columns
-constexpr float kFixed = 1099511627776.f;         // 2^40
-constexpr unsigned long long kNotFinite = 1ull << 63;
+constexpr unsigned long long kNotFinite = 1ull << 63;  // in the fixed-point array
 
 // 221 ring free, 222 ring full / 223 atom free, 224 q_hat / KV full / S free, 225 S full;
 // 226 = 221 + 5: a page id outside the pool
@@ -74,7 +76,9 @@ struct Params {
   int64_t z_tiles;           // chunks of a stream's z
   float* z;                  // [stream][chunk][64 heads][64 rows], segments permuted
   float* part;               // [stream][split][m 64 | l 64]
-  unsigned long long* fixed; // [B][n_cap] (sparse)
+  unsigned long long* fixed; // [B][n_cap] (sparse), in steps of `step` = 1 / fixed_one
+  float fixed_one, slot_max; // slot_max: a little above H, the most that one slot can weigh
+  double step;
   float* acc;
   const uint8_t* tiles;      // q_hat tiles, 128 KB per stream
   float scale2, decay;
@@ -365,8 +369,8 @@ __global__ void __launch_bounds__(kRedThreads) k_mass_sparse(const __grid_consta
   const float w = weight_of(P, bt, j, in, L, part);
   if (!in || threadIdx.x >= kRedRows) return;
   unsigned long long* at = P.fixed + (size_t)b * P.a.n_cap + e;
-  if (w <= 16777216.f) atomicAdd(at, (unsigned long long)__float2ll_rn(w * kFixed));
-  else atomicOr(at, kNotFinite);
+  if (w <= P.slot_max) atomicAdd(at, (unsigned long long)__float2ll_rn(w * P.fixed_one));
+  else atomicOr(at, kNotFinite);  // a NaN
 }
 
 __global__ void __launch_bounds__(kRedThreads) k_mass_finish(const __grid_constant__ Params P) {
@@ -375,7 +379,7 @@ __global__ void __launch_bounds__(kRedThreads) k_mass_finish(const __grid_consta
   if (i >= n) return;
   const unsigned long long f = P.fixed[i];
   const float add = f & kNotFinite ? __uint_as_float(0x7fc00000u)
-                                   : (float)((double)f * 9.094947017729282e-13);  // 2^-40
+                                   : (float)((double)f * P.step);
   P.acc[i] = fmaf(P.decay, P.acc[i], add);
 }
 
@@ -431,6 +435,11 @@ cudaError_t launch_attn_mass(const MqaArgs& a, float decay, float* acc, void* ws
   P.acc = acc;
   P.scale2 = a.scale * 1.44269504088896341f;
   P.decay = decay;
+  int bits = 62;
+  for (int64_t most = 1; most < (int64_t)a.T * a.H; most *= 2) --bits;
+  P.fixed_one = std::ldexp(1.f, bits);
+  P.step = std::ldexp(1.0, -bits);
+  P.slot_max = 1.25f * (float)a.H;  // T slots of it stay below 2^63 steps
   char* tiles = w + pl.z_bytes + pl.part_bytes + pl.fixed_bytes;
   P.tiles = reinterpret_cast<const uint8_t*>(tiles);
   const int64_t streams = (int64_t)a.B * a.T * P.G;

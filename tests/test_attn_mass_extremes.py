@@ -1,9 +1,14 @@
-"""The attention weight per entry at the ends of its range: rows that are not numbers."""
+"""The attention weight per entry at the ends of its range: rows that are not numbers, weights far
+below the largest, sums as large as they can be."""
+import math
+
+import numpy as np
 import pytest
 import torch
 
 import long_context_sparse_08_b200 as csa
 import tests.fp4_util as F
+from tests.fp4_values import C, encode_rows
 
 pytestmark = [pytest.mark.gpu]
 
@@ -68,3 +73,62 @@ def test_sink_beside_rows_that_are_not_numbers():
     P = F.Problem(B=1, pages=3, page_rows=1, n_win=0, seed=33)
     _spoil(P, 0, [0, 1, 2])
     assert torch.isnan(P.mass(torch.zeros((1, 3), device="cuda"))).all()
+
+
+# ------------------------------- small weights, large sums -------------------------------
+
+def _two_kinds(fmt, n, strong, B, T, H, k, log2_ratio, n_win=0):
+    """Entries that hold 1 in dims 128-447 (weak) or 0-127 (strong) under a query that is 2 in dims
+    0-127 after its normalisation: a weak row's weight is 2^-log2_ratio of a strong one's, and only
+    fp32 roundings lie between."""
+    rows = np.zeros((n, C), np.float32)
+    rows[:, 128:448] = 1
+    rows[strong, :128], rows[strong, 128:448] = 1, 0
+    scale = log2_ratio * math.log(2) / 256
+    P = F.Problem(B=B, T=T, H=H, k=k, pages=n, page_rows=1, m=1, n_win=n_win, sink=False, fmt=fmt,
+                  scale=scale, seed=41, pos=[n] * B)
+    order = torch.from_numpy(P.table[0].astype(np.int64)).cuda()
+    data = torch.from_numpy(encode_rows(rows)).cuda() if fmt == "fp4" else \
+        torch.from_numpy(rows).to(torch.bfloat16).cuda()
+    P.pool[order, 0] = data
+    P.q.zero_()
+    P.q[..., :128] = 0.75
+    z = 256 / math.sqrt(1 + 1e-6 / (0.75 ** 2 / 4)) * scale
+    return P, math.exp(-z)
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "bf16"])
+@pytest.mark.parametrize("sparse", [False, True])
+@pytest.mark.parametrize("T,H", [(1, 64), (3, 192)])
+@pytest.mark.parametrize("log2_ratio", [35.0, 41.0, 50.0])
+def test_small_weights_are_kept(fmt, sparse, T, H, log2_ratio):
+    """One strong row and 32 weak ones. An entry's sum over the heads is rounded to steps of
+    2^-(62 - log2(T H)) in a list (at most 2^-52 here, half of it T times: 3 * 2^-53 against
+    3 * 192 * 2^-50, 2^-10.6 of the sum; H = 64 less), a logit of -50 to 2^-19 and its fp32
+    exponential to 2^-21."""
+    P, w = _two_kinds(fmt, 33, [7], 1, T, H, 33 if sparse else 0, log2_ratio)
+    if T > 1:
+        P.q_pos.fill_(33)
+        P.pos[:] = 33
+    if sparse:
+        P.idx = torch.arange(33, dtype=torch.int32, device="cuda").flip(0).expand(1, T, -1).contiguous()
+    got = P.mass(torch.zeros((1, 33), device="cuda")).double().cpu()[0]
+    den = 1 + 32 * w
+    weak = np.delete(got.numpy(), 7)
+    assert np.abs(weak / (T * H * w / den) - 1).max() <= 2.0 ** -10
+    assert abs(float(got[7]) / (T * H / den) - 1) <= 2.0 ** -18
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "bf16"])
+@pytest.mark.parametrize("T,H,copies", [(128, 1024, 1), (683, 192, 1), (3, 64, 4)])
+def test_sums_of_whole_weights(fmt, T, H, copies):
+    """Every query lists one and the same entry: all its weight, T * H in all, the most that the
+    sums of a list have to hold, and exact (a weight of 2^0). Listed four times, each has a weight of
+    2^-2, whose exponent is off by half a step of 3 (2^-23) and its exponential by 2^-22."""
+    P, _ = _two_kinds(fmt, 5, [2], 1, T, H, copies, 1.0)
+    P.q_pos.fill_(5)
+    P.idx = torch.full((1, T, copies), 2, dtype=torch.int32, device="cuda")
+    acc = torch.ones((1, 5), device="cuda")
+    got = P.mass(acc, 0.5).cpu()[0]
+    want = torch.tensor([0.5, 0.5, T * H + 0.5, 0.5, 0.5])
+    assert ((got - want).abs() <= want * (0 if copies == 1 else 2.0 ** -21)).all()
