@@ -148,6 +148,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_mass_logits(const __grid_consta
     if (resolve_rows<kFmt>(rows0, a, x, it, S.ring, kErrRing, [] {}))
       resolve_end(it, S.ring, kErrRing, [] {});
   } else if (warp == 4) {
+    // A CTA without chunks waits for the launch before as well: this grid is not to be over while
+    // that launch still runs, since the next call on the stream writes the tiles anew.
+    if (n == 0) pdl_wait();
     if (n > 0 && elect_one()) {  // one thread issues everything (see attn_fp4.cu)
       const uint32_t idS = idesc_f16(kFmt == kFp4 ? 0 : 1, kQRows, kRows);
       const uint64_t dq = smem_desc(smem_u32(base + kOffQ), 16, 1024, kLayoutSw128);

@@ -1,5 +1,6 @@
 """The attention weight per entry at the ends of its range: rows that are not numbers, weights far
-below the largest, sums as large as they can be."""
+below the largest, sums as large as they can be,
+no rows at all."""
 import math
 
 import numpy as np
@@ -132,3 +133,25 @@ def test_sums_of_whole_weights(fmt, T, H, copies):
     got = P.mass(acc, 0.5).cpu()[0]
     want = torch.tensor([0.5, 0.5, T * H + 0.5, 0.5, 0.5])
     assert ((got - want).abs() <= want * (0 if copies == 1 else 2.0 ** -21)).all()
+
+
+# ------------------------------- no rows -------------------------------
+
+@pytest.mark.parametrize("fmt", ["fp4", "bf16"])
+@pytest.mark.parametrize("k", [0, 3])
+def test_queries_without_any_row_then_with(k, fmt):
+    """No entry visible, no window, no sink (padding of a batch, position -1): the sums only decay.
+    Then, on the same workspace at once, queries that have rows, again and again."""
+    empty = F.Problem(B=70, H=128, k=k, pages=3, page_rows=4, m=4, n_win=0, sink=False, seed=51, fmt=fmt,
+                      pos=[-1] * 70)
+    full = F.Problem(B=70, H=128, k=k, pages=3, page_rows=4, m=4, n_win=0, sink=False, seed=52, fmt=fmt)
+    need = csa.attn_mass_workspace_size(full.p, 70, 1, full.N, 1 if k else 0)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    acc0 = torch.rand((70, full.N), device="cuda")
+    want = full.mass(acc0.clone(), 0.5)
+    for _ in range(20):
+        a, b = acc0.clone(), acc0.clone()
+        empty.mass(a, 0.25, ws=ws)
+        full.mass(b, 0.5, ws=ws)
+        assert torch.equal(a, acc0 * 0.25)
+        assert torch.equal(b, want)
