@@ -38,7 +38,9 @@ __global__ void __launch_bounds__(256) k_q_tiles(const __grid_constant__ QParams
   pdl_wait();
   pdl_trigger();
   const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + gh0 * kC);
-  uint4 raw[2] = {__ldg(src + lane), __ldg(src + lane + 32)};
+  // (plain loads: q may be the work of the launch before, beside whose end this kernel starts, and
+  // the read-only path is for data that no one writes while the kernel runs)
+  uint4 raw[2] = {src[lane], src[lane + 32]};
   float w[16];
 #pragma unroll
   for (int half = 0; half < 2; ++half)
@@ -61,8 +63,8 @@ __global__ void __launch_bounds__(256) k_q_tiles(const __grid_constant__ QParams
   for (int i = 0; i < kPer; ++i) {
     const uint4 cur[2] = {raw[0], raw[1]};
     if (i + 1 < kPer) {
-      raw[0] = __ldg(src + (i + 1) * (kC / 8) + lane);
-      raw[1] = __ldg(src + (i + 1) * (kC / 8) + lane + 32);
+      raw[0] = src[(i + 1) * (kC / 8) + lane];
+      raw[1] = src[(i + 1) * (kC / 8) + lane + 32];
     }
     float y[16], ss = 0.f;
 #pragma unroll
