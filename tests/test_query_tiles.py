@@ -69,3 +69,28 @@ def test_queries_written_by_the_launch_before(fmt):
             assert torch.equal(accs[i], want[i][1])
             if fmt == "fp4":
                 assert torch.equal(outs[i], want[i][0])
+
+
+MANY = [dict(B=1, T=1024, k=16),                      # the first size at which a warp takes eight heads
+        dict(B=3, T=114, k=9, H=192, weight=True),    # 65664 heads, three groups each
+        dict(B=16, T=65, k=33, n_win=37)]
+
+
+@pytest.mark.parametrize("kw", MANY, ids=str)
+def test_attention_of_many_queries(kw):
+    P = F.Problem(pages=30, page_rows=32, m=4, seed=60, pos=[500 + 90 * b for b in range(kw["B"])], **kw)
+    assert P.B * P.T * P.H >= 65536
+    F.check_attention(P.attention(), P.out64(), str(kw))
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "bf16"])
+@pytest.mark.parametrize("kw", MANY + [dict(B=2, T=512, k=0, pages=3, m=128, pos=[60, 20000])], ids=str)
+def test_weight_of_many_queries(kw, fmt):
+    """The end of a prompt, lists and dense."""
+    d = dict(pages=30, page_rows=32, m=4, seed=61, pos=[500 + 90 * b for b in range(kw["B"])])
+    d.update(kw)
+    P = F.Problem(fmt=fmt, **d)
+    assert P.B * P.T * P.H >= 65536
+    acc = torch.from_numpy(np.random.default_rng(0).random((P.B, P.N)).astype(np.float32)).cuda()
+    before = acc.double().cpu().numpy()
+    check_mass(P.mass(acc.clone(), 0.9), P.mass64(acc, 0.9), before, 0.9, str(kw))
