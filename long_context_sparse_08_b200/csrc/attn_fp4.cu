@@ -612,9 +612,17 @@ __global__ void __launch_bounds__(256) k_attn_fp4_combine(const __grid_constant_
 
 // CTAs per stream: as many as fill the SMs, at most one per chunk of the longest list, at most
 // kMaxSplit, and no more than the largest share needs. With one chunk a CTA the partials (128 KB
-// each, written and read again) can cost more than a second chunk does. One against two chunks a
-// CTA, in us: 80 CTAs with 10 to a stream 14.0 / 15.1, 140 with 10 17.3 / 17.8, 72 with 18 14.2 /
-// 15.1, but 108 with 18 15.9 / 15.6 and 144 with 18 17.3 / 15.9.
+// each, written and read again, the merge in batches of 16 to a stream) can cost more than a second
+// chunk does. One against two chunks a CTA over lists, in us (graph replay, 64 heads):
+//   streams x chunks   3 x 26 14.9 / 14.7   3 x 28 14.6 / 14.9   3 x 32 15.2 / 14.9
+//                      4 x 18 14.0 / 14.8   4 x 20 13.9 / 14.9   4 x 22 15.4 / 15.0   4 x 32 17.5 / 15.4
+//                      5 x 14 13.9 / 14.8   5 x 17 15.5 / 14.7   5 x 24 16.8 / 15.2
+//                      6 x 14 14.4 / 15.0   6 x 17 15.7 / 15.3   6 x 24 17.3 / 16.3
+//                      8 x 14 15.1 / 15.4   8 x 16 16.1 / 15.6   8 x 18 17.6 / 15.7
+//                      1 or 2 x 17 to 32: one is faster by 1 to 0 (60 CTAs and fewer)
+// (2 x and 4 x 64 of 128 heads: the same to 0.3.) So two chunks where there are more than 16 one-chunk
+// partials to a stream, and CTAs for more than 4/7 of the SMs (84 of 148). With 16 and fewer the two
+// lie within 0.5 us of each other up to 120 CTAs.
 int choose_split(const MqaArgs& a) {
   const int64_t streams = (int64_t)a.B * a.T * (a.H / kHg);
   const int64_t rows = a.k > 0 ? a.k : a.n_cap;
@@ -623,7 +631,7 @@ int choose_split(const MqaArgs& a) {
   ns = ns < chunks ? ns : chunks;
   ns = ns < 1 ? 1 : (ns > kMaxSplit ? kMaxSplit : ns);
   int64_t share = (chunks + ns - 1) / ns;
-  if (share == 1 && ns > 16 && streams * ns > 88) share = 2;
+  if (share == 1 && ns > 16 && 7 * streams * ns > 4 * device_sm_count()) share = 2;
   return share > 0 ? (int)((chunks + share - 1) / share) : 1;
 }
 
