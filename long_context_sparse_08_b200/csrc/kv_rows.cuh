@@ -128,14 +128,6 @@ struct AddrRing {
   uint64_t full[kRing], free[kRing];
 };
 
-// The lines of `bytes` bytes at addr towards L2 (one instruction serves 32 rows; the bulk form,
-// one row each, took 80 cycles a row).
-__device__ __forceinline__ void prefetch_l2(uint64_t addr, uint32_t bytes) {
-  for (uint32_t o = 0; o < bytes; o += 128)
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(addr + o));
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(addr + bytes - 1));
-}
-
 // The entries of kRing chunks and their pages, one row of each half chunk per lane: the two
 // dependent round trips (index list, page table) are shared by four chunks.
 struct RowBatch {
@@ -229,7 +221,8 @@ __device__ __forceinline__ bool resolve_rows(RowBatch& rb, const MqaArgs& a, con
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.full[rs]);
       // towards L2 while the gather warps are still chunks behind; one instruction serves 32
-      // rows (the bulk form, one row each, took 80 cycles a row)
+      // rows (the bulk form, one row each, took 80 cycles a row). A line per 128 bytes from the row's
+      // start: a 368-byte row that reaches into a fourth line fetches that one with the gather.
       if (j > x.c0) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
