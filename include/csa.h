@@ -71,7 +71,10 @@ typedef enum {
                                 ((c-r)/2 bytes, element 2j in the low nibble), one e8m0 exponent
                                 floor(log2 amax) - 2 per 32 of them, held to [-14, 13] and padded
                                 with zero bytes to a multiple of 16, then the last r (RoPE)
-                                values as bf16. 368 bytes at c = 512, r = 64; r a multiple of 32 */
+                                values as bf16. 368 bytes at c = 512, r = 64; r a multiple of 32.
+                                e2m1 has no infinity and no NaN: larger values become 6 * 2^13 with
+                                their sign, and a NaN +6 of its block's scale (RoPE values keep
+                                theirs) */
 } csa_dtype;
 
 /* Method constants, passed by pointer, read on the host during the call only. */
@@ -380,11 +383,10 @@ csa_status csa_index_topk_paged(const csa_params* p, int32_t B, int32_t T,
  * fp32 (q_hat enters the products as two 16-bit parts: 16 bits of it over bf16 rows; 22 bits over
  * 4-bit rows, with f16's range as in the attention); an entry's sum over a call's lists is exact in
  * steps of 2^-62 of T * n_heads rounded up to a power of two (2^-56 for one query of 64 heads). The
- * same inputs give the same bits. decay in
- * [0, 1]. c = 512, rope_dims = 64, n_heads a multiple of 64 and at most 8192, B * T <= 65535 and
- * T * n_heads <= 2^22. With B * T = 0 acc is left as it is. Pages and evicted pages as in the attention (device
- * error code 226). Workspace: csa_attn_mass_workspace_size (sparse = 1 with an index list):
- * 4 bytes per (query, head, row).
+ * same inputs give the same bits. decay in [0, 1]. c = 512, rope_dims = 64, n_heads a multiple of 64
+ * and at most 8192, B * T <= 65535 and T * n_heads <= 2^22. With B * T = 0 acc is left as it is.
+ * Pages and evicted pages as in the attention (device error code 226). Workspace:
+ * csa_attn_mass_workspace_size (sparse = 1 with an index list): 4 bytes per (query, head, row).
  */
 csa_status csa_attn_mass_paged(const csa_params* p, int32_t B, int32_t T, const void* q,
                                const int64_t* q_pos, const csa_paged_kv* kv, const int32_t* idx,
@@ -404,9 +406,10 @@ size_t csa_attn_mass_workspace_size(const csa_params* p, int32_t B, int32_t T, i
  *   new_table int32 [B, max_pages]: page_table with -2 at the evicted pages (it may be
  *     page_table itself);
  *   kept int32 [B, budget]: the kept logical pages, ascending, then -1;
- *   entries int32 [B, budget * page_rows] or NULL: their entries, ascending, then -1: the index
- *     list with which csa_sparse_mqa_paged attends to what is left (p->topk = budget *
- *     page_rows, at most 2048);
+ *   entries int32 [B, budget * page_rows] or NULL: their entries, ascending, then -1. Up to 2048
+ *     of them are an index list with which csa_sparse_mqa_paged attends to what is left (p->topk =
+ *     budget * page_rows); longer lists are for the caller's own use, and hca_dense_mqa_paged over
+ *     new_table attends to what is left;
  *   evicted int32 [B, max_pages]: the evicted logical pages, ascending, then -1;
  *   counts int32 [B, 3]: kept pages, their entries, evicted pages.
  * Entries keep their numbers, and nothing is moved. On the host, csa_page_alloc_evict gives the
@@ -483,7 +486,7 @@ csa_status csa_state_resume(const csa_params* p, csa_dtype io, int32_t B, int64_
  *     back and marks them -2 (evicted); reserve does not map them again. All or nothing.
  *   csa_page_alloc_table: the host table [B, max_pages] (valid until destroy).
  *   csa_page_alloc_free_pages / csa_page_alloc_mapped: free pages in the pool / logical pages
- *     mapped for request b (-1 for an invalid handle or b).
+ *     reserved for request b, those evicted since among them (-1 for an invalid handle or b).
  *   csa_state_pages_needed: logical pages that hold the entries of a request's first n_tok
  *     tokens, ceil(floor(n_tok / m) / page_rows); reserving that many before appending the
  *     token at position n_tok - 1 maps the page its entry goes to (-1 for invalid sizes).

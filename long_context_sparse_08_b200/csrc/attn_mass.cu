@@ -26,12 +26,17 @@
 // products are done, so the gather warps refill the first while the others are multiplied. A
 // chunk's logits leave as one bulk copy of 16 KB from a staged tile.
 //
-// What bounds it: as the attention, operands from shared memory (6 KB and 48 cycles for each 16
-// of K), then the logits, 4 bytes per (query, head, row) written and read once more (34 MB each
-// way for 16 queries x 64 heads over 8192 entries: mostly L2). Measured, whole call: that case
-// 46.1 us, 3 queries over 600 bf16 entries 10.1 us, 4 x 4 queries x 128 heads with lists of 1024
-// 25.4 us. Keeping the logits beats a second product over the rows once the maxima are known,
-// which would cost another 28 us in the first case where they cost 10.
+// What bounds it: the chain gather -> product -> read over the one KV buffer (the products' operands
+// from shared memory, 6 KB and 48 cycles for each 16 of K, and the gather's stores are half of a
+// chunk's time), then the logits, 4 bytes per (query, head, row) written and read once more (28 MB
+// each way for 16 queries x 64 heads over 5350 to 8191 entries: mostly L2). Measured, calls one after
+// another: that case 46.1 us, 3 queries over 600 bf16 entries 11.2 us, 4 x 4 queries x 128 heads
+// with lists of 1024 26.0 us. Keeping the logits beats a second product over the rows once the maxima
+// are known, which would cost another 28 us in the first case where they cost 10.
+//
+// Roundings: q_hat to the two parts; the tensor cores' sums of 512 products are fp32 and cut off, about
+// 1e-6 of a weight at logits of 5 to 9 (the weights of a row beside larger ones come out that much
+// high); exponents, maxima and sums are fp32.
 #include <cmath>
 
 #include "common.cuh"

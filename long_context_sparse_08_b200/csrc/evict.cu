@@ -16,8 +16,9 @@
 // 4 bytes are read per entry and a few per page, so latencies bound it. One CTA with the keys at
 // hand beat a cluster of eight per request (18 to 40 us: seven cluster barriers and sums
 // through distributed shared memory) and a CTA that read the keys from L2 in every pass (26 us).
-// Measured: 16 requests of 8192 one-entry pages 12.8 us, 4 of 8192 pages of 32 entries (lists of
-// 64000 entries written) 17.6 us, one of 600 pages 5.3 us.
+// Measured, calls one after another: 16 requests of 8192 one-entry pages 12.6 to 13.6 us, 4 of 8192
+// pages of 32 entries (lists of 64000 entries written) 17.6 us, one of 600 pages 6.8 us (replayed
+// from a graph 12.7, 17.6 and 5.2 us).
 #include "common.cuh"
 #include "host_util.cuh"
 #include "internal.h"
